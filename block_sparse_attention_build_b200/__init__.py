@@ -1,4 +1,5 @@
-"""Block-sparse causal attention forward and backward on B200 (sm_100a).
+"""Block-sparse causal attention forward and backward on B200 (sm_100a), and
+the rotation, paged cache and cached attention that serve with it (``cached``).
 
 Thin binding over the C ABI in ``include/sparse_attn.h`` (``libsparse_attn.so``,
 built in-tree).  This module only marshals arguments: torch tensors supply
@@ -45,6 +46,8 @@ EXPORTED = (
     "sparse_attn_transpose_block_mask", "sparse_attn_bwd_workspace", "sparse_attn_bwd",
     "sparse_attn_stride_plan", "sparse_attn_fwd_stride_workspace", "sparse_attn_fwd_stride",
     "sparse_attn_bwd_heads",
+    "sparse_attn_rotary", "sparse_attn_cache_append", "sparse_attn_fwd_cached", "sparse_attn_fwd_shared",
+    "sparse_attn_fwd_cached_workspace", "sparse_attn_fwd_shared_workspace",
 )
 
 
@@ -512,3 +515,7 @@ def set_debug(flags: int = 0, timeout_cycles: int = 0) -> None:
 
 def version() -> int:
     return int(lib.sparse_attn_version())
+
+
+from .cached import (CacheBatch, KVCache, Rotary, cache_append, fwd_cached, fwd_cached_workspace_bytes,  # noqa: E402
+                     fwd_shared, fwd_shared_workspace_bytes, rotary, rotary_bwd)

@@ -1,0 +1,326 @@
+"""Rotary positions, the paged key/value cache and attention over it.
+
+Thin binding like the rest of the package: objects here only hold torch tensors and the C
+structures that describe them.
+
+    spec = Rotary([10000.0 ** (-i / 64) for i in range(64)])
+    cache = KVCache(k_pages, v_pages)                       # [n_pages, Hkv, page_size, D] bf16
+    batch = CacheBatch(q_start, kv_len, table, max_q=1)     # int32, on the device
+    q = cache_append(k, v, cache, batch, rotary=spec, q=q)  # k, v [T, Hkv, D], q [T, Hq, D]
+    o, lse = fwd_cached(q, cache, batch, Pattern(window=1024, sinks=4))
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import EXPORTED, Pattern, _check, _Pattern, _Shape, _stream_handle, lib
+
+
+class _View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+class _Rotary(ctypes.Structure):
+    _fields_ = [("n_pairs", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("freq", ctypes.c_void_p), ("axis", ctypes.c_void_p)]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+class _CacheBatch(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int64), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p)]
+
+
+def _declare() -> None:
+    i32, i64, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+    V, C, B = ctypes.POINTER(_View), ctypes.POINTER(_KVCache), ctypes.POINTER(_CacheBatch)
+    R, P, S = ctypes.POINTER(_Rotary), ctypes.POINTER(_Pattern), ctypes.POINTER(_Shape)
+    lib.sparse_attn_rotary.argtypes = [V, V, vp, i64, i64, R, S, i32, V, V, vp]
+    lib.sparse_attn_cache_append.argtypes = [V, V, C, B, R, vp, i64, i32, V, V, i32, vp]
+    lib.sparse_attn_fwd_cached.argtypes = [V, C, B, P, i32, ctypes.c_float, V, vp, vp, sz, vp]
+    lib.sparse_attn_fwd_shared.argtypes = [V, C, B, vp, i32, P, i32, ctypes.c_float, V, vp, vp, sz, vp]
+    for f in ("sparse_attn_fwd_cached_workspace", "sparse_attn_fwd_shared_workspace"):
+        getattr(lib, f).argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
+    for f in EXPORTED[EXPORTED.index("sparse_attn_rotary"):]:
+        getattr(lib, f).restype = ctypes.c_int
+
+
+_declare()
+
+
+def _bf16_rows(where: str, name: str, t, dims: int, device=None) -> None:
+    """A bf16 CUDA tensor of `dims` dimensions whose rows are contiguous."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != dims or t.stride(-1) != 1:
+        raise TypeError(f"{where}: {name} must be a {dims}-dimensional bf16 CUDA tensor with contiguous rows")
+    if device is not None and t.device != device:
+        raise TypeError(f"{where}: {name} is on {t.device}, not on {device}")
+
+
+def _int32(where: str, name: str, t, dims: int, device) -> None:
+    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise TypeError(f"{where}: {name} must be a {dims}-dimensional int32 CUDA tensor with contiguous rows")
+    if t.device != device:
+        raise TypeError(f"{where}: {name} is on {t.device}, not on {device}")
+
+
+def _same_shape(where: str, name: str, t, shape) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{where}: {name} has the shape {tuple(t.shape)}, not {tuple(shape)}")
+
+
+def _tokens(t) -> _View:
+    """View of a tensor of tokens [T, H, D]."""
+    return _View(t.data_ptr(), 0, t.stride(1), t.stride(0))
+
+
+def _sequences(t) -> _View:
+    """View of whole sequences [B, H, N, D]."""
+    return _View(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+
+
+class Rotary:
+    """Which pairs of a row turn, how fast (radians a position) and along which axis of the
+    position.  ``freq`` holds one number per pair; ``axis`` one index per pair (default 0).
+    Pairs are elements (j, j + len(freq)) or, ``interleaved``, (2j, 2j + 1); elements behind the
+    last pair stay."""
+
+    def __init__(self, freq, axis=None, interleaved: bool = False, n_axes: int | None = None):
+        freq = [float(f) for f in freq]
+        if axis is not None:
+            axis = [int(a) for a in axis]
+            if len(axis) != len(freq):
+                raise ValueError("one axis per frequency")
+        self.n_axes = n_axes if n_axes is not None else (max(axis) + 1 if axis else 1)
+        self.n_pairs, self.interleaved = len(freq), bool(interleaved)
+        self._freq = (ctypes.c_double * max(len(freq), 1))(*freq)
+        self._axis = (ctypes.c_int32 * max(len(axis), 1))(*axis) if axis is not None else None
+        self._struct = _Rotary(len(freq), self.n_axes, int(self.interleaved), ctypes.addressof(self._freq),
+                               ctypes.addressof(self._axis) if axis is not None else None)
+
+
+class KVCache:
+    """Keys and values in pages: two bf16 CUDA tensors [n_pages, Hkv, page_size, D] of equal
+    strides (any order of heads and places in memory; rows of D contiguous)."""
+
+    def __init__(self, k_pages, v_pages):
+        _bf16_rows("KVCache", "k_pages", k_pages, 4)
+        _bf16_rows("KVCache", "v_pages", v_pages, 4, k_pages.device)
+        if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
+            raise ValueError("KVCache: k_pages and v_pages differ in shape or strides")
+        self.k, self.v = k_pages, v_pages
+        n, self.Hkv, self.page_size, self.D = k_pages.shape
+        st = k_pages.stride()
+        self._struct = _KVCache(k_pages.data_ptr(), v_pages.data_ptr(), n, self.page_size, self.Hkv, self.D, st[0],
+                                st[1], st[2])
+
+    @property
+    def device(self):
+        return self.k.device
+
+
+class CacheBatch:
+    """A batch over a cache: ``q_start`` [B + 1] rows of the token tensors where each sequence's
+    new tokens begin (ascending from 0), ``kv_len`` [B] cached tokens (new ones included),
+    ``table`` [B, max_pages] pages.  int32 CUDA tensors; their contents are read when a kernel
+    runs, so a captured graph follows them.  ``max_q``: most new tokens of one sequence, as far as
+    known; it only chooses between kernels."""
+
+    def __init__(self, q_start, kv_len, table, max_q: int | None = None):
+        dev = q_start.device
+        _int32("CacheBatch", "q_start", q_start, 1, dev)
+        _int32("CacheBatch", "kv_len", kv_len, 1, dev)
+        _int32("CacheBatch", "table", table, 2, dev)
+        B = kv_len.shape[0]
+        if q_start.shape[0] != B + 1 or table.shape[0] != B:
+            raise ValueError("CacheBatch: q_start [B + 1], kv_len [B] and table [B, max_pages] disagree on B")
+        self.q_start, self.kv_len, self.table, self.max_q = q_start, kv_len, table, max_q
+        self._struct = _CacheBatch(B, 0, max_q or 0, table.shape[1], table.stride(0) if B > 1 else table.shape[1],
+                                   q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr())
+
+    @property
+    def device(self):
+        return self.q_start.device
+
+    def _c(self, T: int) -> _CacheBatch:
+        s = self._struct
+        return _CacheBatch(s.B, T, s.max_q, s.max_pages, s.table_stride, s.q_start, s.kv_len, s.table)
+
+
+def _rotate(where, q, k, positions, spec, backward, q_out, k_out, stream):
+    _bf16_rows(where, "q", q, 4)
+    B, Hq, N, D = q.shape
+    dev = q.device
+    _int32(where, "positions", positions, 3, dev)
+    if tuple(positions.shape) not in ((spec.n_axes, B, N), (spec.n_axes, 1, N)):
+        raise ValueError(f"{where}: positions must be [{spec.n_axes}, {B} or 1, {N}]")
+    pairs = [("q", q, q_out)]
+    if k is not None:
+        _bf16_rows(where, "k", k, 4, dev)
+        _same_shape(where, "k", k, (B, k.shape[1], N, D))
+        pairs.append(("k", k, k_out))
+    elif k_out is not None:
+        raise ValueError(f"{where}: k_out without k")
+    outs, views = [], []
+    for name, x, out in pairs:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        else:
+            _bf16_rows(where, name + "_out", out, 4, dev)
+            _same_shape(where, name + "_out", out, x.shape)
+        outs.append(out)
+        views.append((_sequences(x), _sequences(out)))
+    shape = _Shape(B, Hq, k.shape[1] if k is not None else 0, N, D)
+    ref = ctypes.byref
+    kv = (ref(views[1][0]), ref(views[1][1])) if k is not None else (None, None)
+    with torch.cuda.device(dev):
+        st = _stream_handle(stream, dev)
+        _check(lib.sparse_attn_rotary(ref(views[0][0]), kv[0], positions.data_ptr(), positions.stride(0),
+                                      positions.stride(1) if positions.shape[1] > 1 else 0, ref(spec._struct),
+                                      ref(shape), backward, ref(views[0][1]), kv[1], st), "sparse_attn_rotary")
+    return outs[0], (outs[1] if k is not None else None)
+
+
+def rotary(q, k, positions, spec: Rotary, q_out=None, k_out=None, stream=None):
+    """(q', k') rotated by their positions.  q [B, Hq, N, D], k [B, Hkv, N, D] (or None), bf16 CUDA
+    tensors with contiguous rows, any other strides; positions int32 [n_axes, B, N] or
+    [n_axes, 1, N].  An output may be its input.  Asynchronous on ``stream``."""
+    return _rotate("rotary", q, k, positions, spec, 0, q_out, k_out, stream)
+
+
+def rotary_bwd(dq, dk, positions, spec: Rotary, q_out=None, k_out=None, stream=None):
+    """Gradients of ``rotary``'s inputs from those of its outputs (the rotation by the negated
+    angles).  Arguments as ``rotary``."""
+    return _rotate("rotary_bwd", dq, dk, positions, spec, 1, q_out, k_out, stream)
+
+
+def cache_append(k, v, cache: KVCache, batch: CacheBatch, rotary: Rotary | None = None, positions=None,
+                 pos_offset: int = 0, q=None, q_out=None, stream=None):
+    """Write the new tokens' keys and values [T, Hkv, D] to their places in the cache, keys rotated
+    by ``rotary`` on the way.  With ``q`` [T, Hq, D] the queries are rotated in the same launch and
+    returned (in ``q_out`` if given, which may be ``q``).  ``positions`` int32 [n_axes, T] replaces
+    the tokens' positions in the cache (+ ``pos_offset``).  Asynchronous on ``stream``."""
+    where = "cache_append"
+    dev = cache.device
+    T = k.shape[0]
+    for name, x in (("k", k), ("v", v)):
+        _bf16_rows(where, name, x, 3, dev)
+        _same_shape(where, name, x, (T, cache.Hkv, cache.D))
+    if batch.device != dev:
+        raise TypeError(f"{where}: batch is on {batch.device}, not on {dev}")
+    pos_ptr, pos_stride = None, 0
+    if positions is not None:
+        if rotary is None:
+            raise ValueError(f"{where}: positions without rotary")
+        _int32(where, "positions", positions, 2, dev)
+        _same_shape(where, "positions", positions, (rotary.n_axes, T))
+        pos_ptr, pos_stride = positions.data_ptr(), positions.stride(0)
+    qv = ov = None
+    Hq = 0
+    if q is not None:
+        if rotary is None:
+            raise ValueError(f"{where}: q without rotary")
+        _bf16_rows(where, "q", q, 3, dev)
+        Hq = q.shape[1]
+        _same_shape(where, "q", q, (T, Hq, cache.D))
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        else:
+            _bf16_rows(where, "q_out", q_out, 3, dev)
+            _same_shape(where, "q_out", q_out, q.shape)
+        qv, ov = ctypes.byref(_tokens(q)), ctypes.byref(_tokens(q_out))
+    elif q_out is not None:
+        raise ValueError(f"{where}: q_out without q")
+    ref = ctypes.byref
+    with torch.cuda.device(dev):
+        st = _stream_handle(stream, dev)
+        _check(lib.sparse_attn_cache_append(ref(_tokens(k)), ref(_tokens(v)), ref(cache._struct), ref(batch._c(T)),
+                                            ref(rotary._struct) if rotary is not None else None, pos_ptr, pos_stride,
+                                            int(pos_offset), qv, ov, Hq, st), "sparse_attn_cache_append")
+    return q_out
+
+
+def _workspace(fn: str, T: int, Hq: int, Hkv: int, D: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(getattr(lib, fn)(T, Hq, Hkv, D, ctypes.byref(n)), fn)
+    return n.value
+
+
+def fwd_cached_workspace_bytes(T: int, Hq: int, Hkv: int, D: int) -> int:
+    return _workspace("sparse_attn_fwd_cached_workspace", T, Hq, Hkv, D)
+
+
+def fwd_shared_workspace_bytes(T: int, Hq: int, Hkv: int, D: int) -> int:
+    return _workspace("sparse_attn_fwd_shared_workspace", T, Hq, Hkv, D)
+
+
+def _attend(fn, q, cache, batch, prefix, pattern, scale, out, lse, workspace, stream):
+    where = fn[len("sparse_attn_"):]
+    dev = cache.device
+    _bf16_rows(where, "q", q, 3, dev)
+    T, Hq, D = q.shape
+    _same_shape(where, "q", q, (T, Hq, cache.D))
+    if batch.device != dev:
+        raise TypeError(f"{where}: batch is on {batch.device}, not on {dev}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _bf16_rows(where, "out", out, 3, dev)
+        _same_shape(where, "out", out, q.shape)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    elif lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous() or tuple(lse.shape) != (T, Hq):
+        raise TypeError(f"{where}: lse must be a contiguous fp32 tensor [T, Hq] on {dev}")
+    with torch.cuda.device(dev):
+        st = _stream_handle(stream, dev)
+        if workspace is None:
+            # taken on the stream that uses it, so that it is not handed out again before the kernels are done
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+                workspace = torch.empty(max(_workspace(fn + "_workspace", T, Hq, cache.Hkv, D), 1),
+                                        dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise TypeError(f"{where}: workspace must be a contiguous tensor on {dev}")
+        ref = ctypes.byref
+        _check(getattr(lib, fn)(ref(_tokens(q)), ref(cache._struct), ref(batch._c(T)), *prefix, ref(pattern._c()), Hq,
+                                float(scale if scale is not None else 1.0 / math.sqrt(D)), ref(_tokens(out)),
+                                lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                st), fn)
+    return out, lse
+
+
+def fwd_cached(q, cache: KVCache, batch: CacheBatch, pattern: Pattern, scale: float | None = None, out=None, lse=None,
+               workspace=None, stream=None):
+    """Attention of new tokens q [T, Hq, D] over the cache: O [T, Hq, D] bf16 and LSE [T, Hq] fp32.
+
+    ``pattern`` is causal with window, sinks and n_global.  Rows of no sequence keep what ``out``
+    and ``lse`` held.  ``workspace``: at least ``fwd_cached_workspace_bytes`` bytes, not shared by
+    calls that may run at the same time.  Asynchronous on ``stream``."""
+    return _attend("sparse_attn_fwd_cached", q, cache, batch, (), pattern, scale, out, lse, workspace, stream)
+
+
+def fwd_shared(q, cache: KVCache, batch: CacheBatch, prefix_table, prefix_len: int, pattern: Pattern,
+               scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
+    """``fwd_cached`` for sequences that all begin with one prefix of ``prefix_len`` tokens in the
+    pages ``prefix_table`` (int32 CUDA tensor), read once for all of them.  ``batch`` describes what
+    follows the prefix.  ``workspace``: at least ``fwd_shared_workspace_bytes`` bytes."""
+    prefix_len = int(prefix_len)
+    if prefix_table is None:
+        if prefix_len:
+            raise ValueError("fwd_shared: prefix_len without prefix_table")
+        ptr = None
+    else:
+        _int32("fwd_shared", "prefix_table", prefix_table, 1, cache.device)
+        if prefix_len > prefix_table.shape[0] * cache.page_size:
+            raise ValueError("fwd_shared: prefix_table holds fewer than prefix_len tokens")
+        ptr = prefix_table.data_ptr()
+    return _attend("sparse_attn_fwd_shared", q, cache, batch, (ptr, prefix_len), pattern, scale, out, lse, workspace,
+                   stream)

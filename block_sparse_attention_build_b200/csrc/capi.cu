@@ -273,6 +273,18 @@ int fwd_impl(const void* Q, const void* K, const void* V, const sa_block_mask* m
     return launch_any<true>(s.D, mask->block, mq, mk, mv, mo, p, hp, g, st);
 }
 
+// An address that device `dev` can read: its own memory, managed or pinned host memory.
+bool readable_on(const void* a, int dev)
+{
+    cudaPointerAttributes at;
+    if (cudaPointerGetAttributes(&at, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return false;
+    }
+    return (at.type == cudaMemoryTypeDevice && at.device == dev) || at.type == cudaMemoryTypeManaged ||
+           at.type == cudaMemoryTypeHost;
+}
+
 }  // namespace
 
 int device_status_word(int32_t** out) { return status_word(out); }
@@ -313,18 +325,19 @@ int check_device_mask(const sa_block_mask* m)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SA_ERR_CUDA;
     const void* arrays[3] = {m->kv_count, m->kv_index, m->kv_full};
-    for (const void* a : arrays) {
-        cudaPointerAttributes at;
-        if (cudaPointerGetAttributes(&at, a) != cudaSuccess) {
-            (void)cudaGetLastError();
-            return SA_ERR_INVALID_ARG;
-        }
-        const bool ok = (at.type == cudaMemoryTypeDevice && at.device == dev) || at.type == cudaMemoryTypeManaged ||
-                        at.type == cudaMemoryTypeHost;
-        if (!ok) return SA_ERR_INVALID_ARG;
-    }
+    for (const void* a : arrays)
+        if (!readable_on(a, dev)) return SA_ERR_INVALID_ARG;
     return SA_OK;
 }
+
+int check_device_array(const void* a)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SA_ERR_CUDA;
+    return readable_on(a, dev) ? SA_OK : SA_ERR_INVALID_ARG;
+}
+
+int check_pattern(const sa_pattern& pt) { return pattern_status(pt); }
 
 }  // namespace sa
 

@@ -25,4 +25,11 @@ int check_host_mask(const sa_block_mask* m, int64_t T);
 // SA_ERR_INVALID_ARG, or SA_ERR_CUDA when the device query fails.
 int check_device_mask(const sa_block_mask* m);
 
+// The same for one array.
+int check_device_array(const void* a);
+
+// The checks every entry point makes of a pattern's fields: SA_OK,
+// SA_ERR_INVALID_ARG or SA_ERR_UNSUPPORTED.
+int check_pattern(const sa_pattern& pt);
+
 }  // namespace sa

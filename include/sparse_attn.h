@@ -388,6 +388,153 @@ int sparse_attn_fwd_stride(const void* Q, const void* K, const void* V, const sa
                            const sa_block_mask* pass2, const sa_pattern* pattern, const sa_shape* shape, float scale,
                            void* O, float* LSE, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- rotary positions and the paged cache ---------------------------------- */
+
+/*
+ * A bf16 tensor given by strides (in elements; the D elements of a row are
+ * contiguous): element (b, h, t, d) at data + b * batch_stride + h * head_stride
+ * + t * token_stride + d.  data is 16-byte aligned and the strides are multiples
+ * of 8 elements (else SA_ERR_MISALIGNED) and not negative.  Tensors of tokens
+ * [T, H, D] have no batch (batch_stride is not read).  A tensor that is written
+ * may not repeat a stride of 0 over an extent above 1 (SA_ERR_INVALID_ARG).
+ */
+typedef struct {
+    void* data;
+    int64_t batch_stride, head_stride, token_stride;
+} sa_view;
+
+/*
+ * Rotation of pairs of a row's elements by its position.  Pair j < n_pairs turns
+ * by the angle pos[axis[j]] * freq[j]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * where (a, b) are elements (2j, 2j + 1) when interleaved is 1 and elements
+ * (j, j + n_pairs) when it is 0; elements 2 n_pairs .. D - 1 stay as they are.
+ * A position has n_axes components (time, height, width, ...; 1 for text).  The
+ * angle is a 64-bit product reduced to a turn, so positions far from 0 lose
+ * nothing; sine, cosine and the rotation are taken in 32 bits and rounded once.
+ * Host arrays, read before the call returns: freq [n_pairs] finite radians per
+ * position, axis [n_pairs] in [0, n_axes), or NULL for axis 0 throughout.
+ * 0 <= 2 n_pairs <= D, 1 <= n_axes <= 4, interleaved 0 or 1 (else
+ * SA_ERR_INVALID_ARG).
+ */
+typedef struct {
+    int32_t n_pairs, n_axes, interleaved;
+    const double* freq;
+    const int32_t* axis;
+} sa_rotary;
+
+/*
+ * Rotate queries and keys of whole sequences (shape B, Hq, Hkv, N, D; D 64 or
+ * 128) into q_out, k_out, in one launch on `stream`; k and k_out are both NULL
+ * to rotate q alone (Hkv is then not read).  positions: device int32, component
+ * a of token t of sequence b at positions[a * pos_axis_stride + b *
+ * pos_batch_stride + t] (a batch stride of 0 gives all sequences the same).
+ * backward = 1 turns by the negated angles: with dq', dk' the gradients of the
+ * rotated tensors, the call gives those of q and k.  An output may be its own
+ * input (same data and strides); otherwise outputs overlap nothing.  Returns
+ * without waiting.
+ */
+int sparse_attn_rotary(const sa_view* q, const sa_view* k, const int32_t* positions, int64_t pos_axis_stride,
+                       int64_t pos_batch_stride, const sa_rotary* rotary, const sa_shape* shape, int32_t backward,
+                       const sa_view* q_out, const sa_view* k_out, void* stream);
+
+/*
+ * A cache of keys and values in pages of page_size tokens (16, 32, 64, 128 or
+ * 256; else SA_ERR_UNSUPPORTED): element d of head h of place i of page p at
+ * k + p * page_stride + h * head_stride + i * token_stride + d, and the same in
+ * v.  Device memory, bf16, alignment as sa_view; strides are positive.  The
+ * order of heads and places within a page is free (heads outside or inside).
+ */
+typedef struct {
+    void* k;
+    void* v;
+    int32_t n_pages, page_size, Hkv, D;
+    int64_t page_stride, head_stride, token_stride;
+} sa_kv_cache;
+
+/*
+ * A batch of B sequences over a cache; q_start, kv_len and table are device
+ * memory (checked as a block mask's arrays), so that a captured graph follows
+ * their contents from replay to replay.
+ *   q_start [B + 1]  the new tokens of sequence b are rows q_start[b] ..
+ *                    q_start[b + 1] - 1 of the token tensors; ascending from 0
+ *   kv_len  [B]      tokens of sequence b in the cache, its new ones included
+ *                    (0 for a padded sequence)
+ *   table   [B, max_pages], row stride table_stride: page of tokens i *
+ *                    page_size .. of sequence b at table[b * table_stride + i]
+ *   T                rows of the token tensors; rows q_start[B] .. T - 1 belong
+ *                    to no sequence, are not read and keep their outputs
+ *   max_q            most new tokens of one sequence as far as the host knows (0:
+ *                    unknown); chooses between kernels, results hold for any value
+ * Row i of sequence b stands at position kv_len[b] - (its new tokens) + i.  A
+ * kv_len above max_pages * page_size is read as that.  Table entries beyond a
+ * sequence's length are not read; a page outside [0, n_pages) holds keys and
+ * values of zero and takes no writes.
+ */
+typedef struct {
+    int32_t B, T, max_q, max_pages;
+    int64_t table_stride;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* table;
+} sa_cache_batch;
+
+/*
+ * Write a batch's new keys and values [T, Hkv, D] to their places in the cache,
+ * the keys rotated on the way (rotary NULL: as they are), and, unless q is NULL,
+ * rotate the new queries [T, Hq, D] into q_out; one launch on `stream`.
+ * positions (device int32, component a of token t at positions[a *
+ * pos_axis_stride + t]) gives the rotation's positions; NULL: a token's position
+ * in the cache + pos_offset on every axis (pos_offset is the length of a prefix
+ * held apart, see sparse_attn_fwd_shared).  Tokens whose place lies before 0,
+ * behind the table or on a page outside the cache are not written.  q without
+ * rotary gives SA_ERR_INVALID_ARG.  q_out may be q.  Two tokens of one call never
+ * share a place unless the table repeats a page.  Returns without waiting.
+ */
+int sparse_attn_cache_append(const sa_view* k, const sa_view* v, const sa_kv_cache* cache,
+                             const sa_cache_batch* batch, const sa_rotary* rotary, const int32_t* positions,
+                             int64_t pos_axis_stride, int32_t pos_offset, const sa_view* q, const sa_view* q_out,
+                             int32_t Hq, void* stream);
+
+/* Device workspace bytes of sparse_attn_fwd_cached and sparse_attn_fwd_shared
+ * for T rows (on the current device; that of a B200 where there is none). */
+int sparse_attn_fwd_cached_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t D, size_t* bytes);
+int sparse_attn_fwd_shared_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t D, size_t* bytes);
+
+/*
+ * Attention of a batch's new tokens over the cache (their own keys and values
+ * already appended): row at position p sees key kv when
+ *   kv <= p and (p - kv <= window or kv < sinks or kv < n_global or p < n_global)
+ * (causal == 1 with window, sinks and n_global; other rules give
+ * SA_ERR_UNSUPPORTED).  Any number of new tokens per sequence, from single ones
+ * to whole prompts, mixed freely.
+ *   q, o  [T, Hq, D] bf16 by strides; o does not overlap q
+ *   lse   [T, Hq] fp32 contiguous, natural log; rows that see nothing get O = 0,
+ *         LSE = -inf
+ *   workspace  device memory of at least sparse_attn_fwd_cached_workspace bytes,
+ *         256-byte aligned (SA_ERR_MISALIGNED; SA_ERR_BUFFER_TOO_SMALL), contents
+ *         need not be preserved; not shared by calls that may run at the same time
+ * Asynchronous on `stream`; errors as sparse_attn_fwd.  What the cache holds at
+ * places no row of a sequence sees (infinities and NaN too) does not matter.
+ * Results of the same call on the same inputs are bit-identical.
+ */
+int sparse_attn_fwd_cached(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* batch,
+                           const sa_pattern* pattern, int32_t Hq, float scale, const sa_view* o, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The same for sequences that all begin with one prefix of prefix_len tokens,
+ * held once in the pages prefix_table [ceil(prefix_len / page_size)] (device
+ * memory): the prefix's keys and values are read once for the rows of all
+ * sequences.  kv_len and table describe what follows the prefix, so that place i
+ * of a sequence stands at position prefix_len + i.  prefix_len 0 is
+ * sparse_attn_fwd_cached (prefix_table may then be NULL).
+ */
+int sparse_attn_fwd_shared(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* batch,
+                           const int32_t* prefix_table, int32_t prefix_len, const sa_pattern* pattern, int32_t Hq,
+                           float scale, const sa_view* o, float* lse, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
 const char* sparse_attn_status_string(int status);
 
 /* ABI version: major * 10000 + minor * 100 + patch. */
