@@ -8,13 +8,15 @@
 #include <cstdint>
 
 #include "../../include/sparse_attn.h"
-#include "sm100.cuh"
-#include "cached_sm100.cuh"
+#include "decode_sm100.cuh"
 #include "rotary_sm100.cuh"
 #include "runtime.h"
+#include "tma_host.h"
 
 namespace sa {
 namespace {
+
+constexpr int kMaxDevices = 64;
 
 // One extent of a view and its stride: not negative, whole 16-byte units, and
 // not 0 where a written tensor has more than one element along it.
@@ -237,7 +239,41 @@ extern "C" int sparse_attn_cache_append(const sa_view* k, const sa_view* v, cons
 namespace sa {
 namespace {
 
-size_t cached_bytes(int32_t T, int32_t Hq, int32_t D) { return 256; }
+constexpr int kDecodeCtas = 2;  // CTAs of decode_kernel on one SM
+
+// Workspace: the parts of cut items, where each row's result lies, and, with a
+// prefix, each pass's finished rows.
+struct CachedLayout {
+    size_t part_o, part_ml, info[2], acc[2], acc_ml[2], total;
+    int64_t rows;       // part rows of one pass
+    int64_t part_rows;  // of all passes
+};
+
+CachedLayout cached_layout(int32_t T, int32_t Hq, int32_t D, bool prefix)
+{
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    const int n_sm = device_sm_count() > 0 ? device_sm_count() : 148;
+    CachedLayout w{};
+    w.rows = 2 * int64_t(kDecodeCtas) * n_sm * 32;
+    w.part_rows = w.rows * (prefix ? 2 : 1);
+    const size_t th = size_t(T) * Hq;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t x = at;
+        at += up(bytes);
+        return x;
+    };
+    w.part_o = take(size_t(w.part_rows) * D * 4);
+    w.part_ml = take(size_t(w.part_rows) * 8);
+    for (int i = 0; i < (prefix ? 2 : 1); i++) w.info[i] = take(th * sizeof(RowInfo));
+    if (prefix)
+        for (int i = 0; i < 2; i++) {
+            w.acc[i] = take(th * D * 4);
+            w.acc_ml[i] = take(th * 8);
+        }
+    w.total = at;
+    return w;
+}
 
 int workspace_status(int32_t T, int32_t Hq, int32_t Hkv, int32_t D, size_t* bytes)
 {
@@ -247,9 +283,113 @@ int workspace_status(int32_t T, int32_t Hq, int32_t Hkv, int32_t D, size_t* byte
     return SA_OK;
 }
 
+// Map of a cache's K or V pages for boxes of box_rows places of one head and page:
+// (64 columns, place, column panel, head, page), so that one box lands in shared
+// memory as the panels of a 128-byte-swizzled tile.  Heads and places may come in
+// any order in memory; pages past the end read as zeros.
+bool make_map_pages(CUtensorMap* map, const void* base, const sa_kv_cache& c, uint32_t box_rows, uint32_t panels)
+{
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return false;
+    // a stride along an extent of one is never used; give the map a valid one
+    const uint64_t hs = c.Hkv > 1 ? c.head_stride : c.D, ps = c.n_pages > 1 ? c.page_stride : c.D;
+    cuuint64_t dims[5] = {64, cuuint64_t(c.page_size), cuuint64_t(c.D / 64), cuuint64_t(c.Hkv), cuuint64_t(c.n_pages)};
+    cuuint64_t strides[4] = {cuuint64_t(c.token_stride) * 2, 128, hs * 2, ps * 2};
+    cuuint32_t box[5] = {64, box_rows, panels, 1, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A launch that may be set up while the stream's previous kernel, one of this
+// call's, still runs (it waits for it where it has to).
+template <typename... Args>
+int launch_after(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool overlap,
+                 const Args&... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+template <int D, int MT>
+int launch_decode(const sa_kv_cache& cache, const PassParams& p, bool overlap, cudaStream_t st)
+{
+    using C = DecodeCfg<D, MT>;
+    auto kern = decode_kernel<D, MT>;
+    static bool attr_set[kMaxDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SA_ERR_CUDA;
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+            return SA_ERR_CUDA;
+        attr_set[dev] = true;
+    }
+    CUtensorMap mk, mv;
+    const uint32_t rows = cache.page_size < C::TK ? cache.page_size : C::TK;
+    if (!make_map_pages(&mk, cache.k, cache, rows, D / 64) || !make_map_pages(&mv, cache.v, cache, rows, D / 64))
+        return SA_ERR_CUDA;
+    return launch_after(kern, dim3(kDecodeCtas * device_sm_count()), C::kThreads, C::kSmemBytes, st, overlap, mk, mv,
+                        p);
+}
+
+template <int D>
+int launch_join(const JoinParams& j, bool prefix, cudaStream_t st)
+{
+    const int64_t rows = int64_t(j.T) * j.Hq;
+    const int64_t sms = device_sm_count();
+    const bool few = rows <= 8 * sms;
+    const int64_t blocks = few ? rows : (rows + 7) / 8;
+    const dim3 grid(static_cast<unsigned>(blocks < 8 * sms ? blocks : 8 * sms));
+    auto kern = few ? (prefix ? join_kernel<D, 8, true> : join_kernel<D, 8, false>)
+                    : (prefix ? join_kernel<D, 1, true> : join_kernel<D, 1, false>);
+    return launch_after(kern, grid, 256, 0, st, true, j);
+}
+
+template <int D>
+int run_paged(const sa_kv_cache& cache, PassParams p, JoinParams j, const CachedLayout& w, uint8_t* ws,
+              const int32_t* prefix_table, int32_t max_q, cudaStream_t st)
+{
+    const bool prefix = p.prefix_len > 0;
+    p.rows_above = 0;
+    p.rows_upto = INT_MAX;
+    auto pass = [&](const PassParams& pp, int64_t rows, bool overlap) {
+        return rows <= 16 ? launch_decode<D, 1>(cache, pp, overlap, st) : launch_decode<D, 2>(cache, pp, overlap, st);
+    };
+    if (prefix) {
+        PassParams pp = p;
+        pp.over_prefix = 1;
+        pp.table = prefix_table;
+        pp.table_stride = 0;
+        pp.part_row0 = static_cast<int32_t>(w.rows);
+        pp.part_o = p.part_o + w.rows * D;
+        pp.part_ml = p.part_ml + w.rows;
+        pp.info = reinterpret_cast<RowInfo*>(ws + w.info[1]);
+        pp.acc = reinterpret_cast<float*>(ws + w.acc[1]);
+        pp.acc_ml = reinterpret_cast<float2*>(ws + w.acc_ml[1]);
+        p.acc = reinterpret_cast<float*>(ws + w.acc[0]);
+        p.acc_ml = reinterpret_cast<float2*>(ws + w.acc_ml[0]);
+        if (int rc = pass(pp, int64_t(p.T) * p.group, false)) return rc;
+    }
+    const int64_t rows = int64_t(max_q > 0 ? max_q : (p.T + p.B - 1) / p.B) * p.group;
+    if (int rc = pass(p, rows, prefix)) return rc;
+    return launch_join<D>(j, prefix, st);
+}
+
+int32_t clip_to(int32_t v, int64_t n) { return v > n ? static_cast<int32_t>(n) : v; }
+
 int fwd_paged(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* batch, const int32_t* prefix_table,
-              int32_t prefix_len, const sa_pattern* pattern, int32_t Hq, float scale, const sa_view* o, float* lse,
-              void* workspace, size_t workspace_bytes, size_t need, void* stream)
+              int32_t prefix_len, bool shared, const sa_pattern* pattern, int32_t Hq, float scale, const sa_view* o,
+              float* lse, void* workspace, size_t workspace_bytes, void* stream)
 {
     if (!pattern || Hq < 0 || prefix_len < 0) return SA_ERR_INVALID_ARG;
     if (int rc = cache_status(cache)) return rc;
@@ -260,17 +400,23 @@ int fwd_paged(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* 
     if (prefix_len > INT_MAX / 2) return SA_ERR_UNSUPPORTED;
     const int32_t T = batch->T;
     if (batch->B == 0 || T == 0 || Hq == 0) return SA_OK;
-    if (cache->Hkv == 0 || Hq % cache->Hkv) return SA_ERR_UNSUPPORTED;
+    if (cache->Hkv == 0 || cache->n_pages == 0 || Hq % cache->Hkv) return SA_ERR_UNSUPPORTED;
+    if (int64_t(T) * Hq > INT_MAX / 2) return SA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
     if (prefix_len > 0 && !prefix_table) return SA_ERR_INVALID_ARG;
     if (int rc = view_status(q, 1, Hq, T, false)) return rc;
     if (int rc = view_status(o, 1, Hq, T, true)) return rc;
     if (!lse || !workspace) return SA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return SA_ERR_MISALIGNED;
-    if (workspace_bytes < need) return SA_ERR_BUFFER_TOO_SMALL;
+    // fwd_shared asks for its own size for every prefix_len, 0 too
+    const CachedLayout w = cached_layout(T, Hq, cache->D, shared);
+    if (workspace_bytes < w.total) return SA_ERR_BUFFER_TOO_SMALL;
     if (int rc = device_arrays({batch->q_start, batch->kv_len, batch->table, prefix_len > 0 ? prefix_table : nullptr}))
         return rc;
-    CachedParams p{};
+    int32_t* status = nullptr;
+    if (int rc = device_status_word(&status)) return rc;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    PassParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q->data);
     p.q_token = T > 1 ? q->token_stride : 0;
     p.q_head = Hq > 1 ? q->head_stride : 0;
@@ -278,35 +424,54 @@ int fwd_paged(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* 
     p.o_token = T > 1 ? o->token_stride : 0;
     p.o_head = Hq > 1 ? o->head_stride : 0;
     p.lse = lse;
-    p.k = static_cast<const __nv_bfloat16*>(cache->k);
-    p.v = static_cast<const __nv_bfloat16*>(cache->v);
-    p.page_stride = cache->page_stride;
-    p.head_stride = cache->head_stride;
-    p.token_stride = cache->token_stride;
-    p.n_pages = cache->n_pages;
-    p.page_shift = page_shift_of(cache->page_size);
-    p.max_pages = batch->max_pages;
-    p.table_stride = batch->table_stride;
     p.q_start = batch->q_start;
     p.kv_len = batch->kv_len;
     p.table = batch->table;
-    p.prefix_table = prefix_table;
-    p.prefix_len = prefix_len;
+    p.table_stride = batch->B > 1 ? batch->table_stride : 0;
     p.B = batch->B;
     p.T = T;
     p.Hq = Hq;
+    p.Hkv = cache->Hkv;
     p.group = Hq / cache->Hkv;
-    p.window = pattern->window;
-    p.n_global = pattern->n_global;
-    p.cols = pattern->sinks > pattern->n_global ? pattern->sinks : pattern->n_global;
+    p.n_pages = cache->n_pages;
+    p.page_shift = page_shift_of(cache->page_size);
+    p.max_pages = batch->max_pages;
+    p.prefix_len = prefix_len;
+    // window and columns clipped to the longest possible sequence: the same keys, no overflow
+    const int64_t longest = prefix_len + int64_t(batch->max_pages) * cache->page_size;
+    p.window = clip_to(pattern->window, longest);
+    p.n_global = clip_to(pattern->n_global, longest);
+    p.cols = clip_to(pattern->sinks > pattern->n_global ? pattern->sinks : pattern->n_global, longest);
     p.scale_log2 = scale * 1.44269504088896340736f;
+    p.part_o = reinterpret_cast<float*>(ws + w.part_o);
+    p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
+    p.info = reinterpret_cast<RowInfo*>(ws + w.info[0]);
+    p.status = status;
+    p.timeout = wait_limit_cycles();
+    p.debug_flags = debug_flags();
+    JoinParams j{};
+    j.part_o = p.part_o;
+    j.part_ml = p.part_ml;
+    j.info[0] = p.info;
+    j.o = p.o;
+    j.o_token = p.o_token;
+    j.o_head = p.o_head;
+    j.lse = lse;
+    j.q_start = batch->q_start;
+    j.B = batch->B;
+    j.T = T;
+    j.Hq = Hq;
+    j.part_rows = static_cast<int32_t>(w.part_rows);
+    if (prefix_len > 0) {
+        j.info[1] = reinterpret_cast<const RowInfo*>(ws + w.info[1]);
+        for (int i = 0; i < 2; i++) {
+            j.acc[i] = reinterpret_cast<const float*>(ws + w.acc[i]);
+            j.acc_ml[i] = reinterpret_cast<const float2*>(ws + w.acc_ml[i]);
+        }
+    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const dim3 grid(T, Hq);
-    if (cache->D == 128)
-        cached_plain_kernel<128><<<grid, 128, 0, st>>>(p);
-    else
-        cached_plain_kernel<64><<<grid, 128, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+    return cache->D == 128 ? run_paged<128>(*cache, p, j, w, ws, prefix_table, batch->max_q, st)
+                           : run_paged<64>(*cache, p, j, w, ws, prefix_table, batch->max_q, st);
 }
 
 }  // namespace
@@ -315,14 +480,14 @@ int fwd_paged(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* 
 extern "C" int sparse_attn_fwd_cached_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t D, size_t* bytes)
 {
     if (int rc = sa::workspace_status(T, Hq, Hkv, D, bytes)) return rc;
-    *bytes = sa::cached_bytes(T, Hq, D);
+    *bytes = sa::cached_layout(T, Hq, D, false).total;
     return SA_OK;
 }
 
 extern "C" int sparse_attn_fwd_shared_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t D, size_t* bytes)
 {
     if (int rc = sa::workspace_status(T, Hq, Hkv, D, bytes)) return rc;
-    *bytes = sa::cached_bytes(T, Hq, D);
+    *bytes = sa::cached_layout(T, Hq, D, true).total;
     return SA_OK;
 }
 
@@ -331,8 +496,8 @@ extern "C" int sparse_attn_fwd_cached(const sa_view* q, const sa_kv_cache* cache
                                       void* workspace, size_t workspace_bytes, void* stream)
 {
     if (!batch || !cache) return SA_ERR_INVALID_ARG;
-    return sa::fwd_paged(q, cache, batch, nullptr, 0, pattern, Hq, scale, o, lse, workspace, workspace_bytes,
-                         sa::cached_bytes(batch->T, Hq, cache->D), stream);
+    return sa::fwd_paged(q, cache, batch, nullptr, 0, false, pattern, Hq, scale, o, lse, workspace, workspace_bytes,
+                         stream);
 }
 
 extern "C" int sparse_attn_fwd_shared(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* batch,
@@ -341,6 +506,6 @@ extern "C" int sparse_attn_fwd_shared(const sa_view* q, const sa_kv_cache* cache
                                       size_t workspace_bytes, void* stream)
 {
     if (!batch || !cache) return SA_ERR_INVALID_ARG;
-    return sa::fwd_paged(q, cache, batch, prefix_table, prefix_len, pattern, Hq, scale, o, lse, workspace,
-                         workspace_bytes, sa::cached_bytes(batch->T, Hq, cache->D), stream);
+    return sa::fwd_paged(q, cache, batch, prefix_table, prefix_len, true, pattern, Hq, scale, o, lse, workspace,
+                         workspace_bytes, stream);
 }

@@ -1,0 +1,470 @@
+// What the kernels of attention over a paged cache share: the description of a
+// pass, how its work is cut into items and units and spread over the CTAs, and
+// the kernel that joins the parts of an item that several CTAs computed.
+//
+// A pass computes, for the new tokens of every sequence of a batch (or, over a
+// shared prefix, for all of them as one), O = softmax(scale Q K^T) V over the
+// keys a row sees.  The query heads of one key/value head and the new tokens of
+// a sequence form one column of rows (row = token * group + head of the group):
+// they read the same keys, so each key and value is loaded once for all of them.
+//
+//   item  R consecutive rows of one sequence and key/value head
+//   unit  UK consecutive keys of an item; only units that hold a key some row of
+//         the item sees exist: those of the sinks [0, cols) and those of the band
+//         [first row's position - window, last row's position]
+//
+// All units of a pass, item after item, form one line of U units that the G CTAs
+// cut into G pieces of equal length.  So the work is even for any lengths, few
+// rows over a long cache use all SMs, and nothing about it is decided on the
+// host: lengths are read when the kernel runs and a captured graph follows them.
+// An item that lies inside one piece is finished there.  One that is cut leaves
+// its parts, unnormalised in 32 bits with the rows' running maximum and sum: the
+// CTA in which the item begins writes its part to its "tail" slot, every later one
+// to its "head" slot (a CTA has at most one of each), and join_kernel adds them in
+// the order of the CTAs, so results do not depend on which finished first.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "sm100.cuh"
+
+namespace sa {
+
+// Where a row's result lies (one per row and query head): in n > 0 parts at rows
+// `first`, `second`, `second` + stride, ... of the part arrays, or, n = 0,
+// finished by its CTA.
+struct RowInfo {
+    int32_t first, second, n, stride;
+};
+
+struct PassParams {
+    const __nv_bfloat16* q;
+    int64_t q_token, q_head;
+    __nv_bfloat16* o;
+    int64_t o_token, o_head;
+    float* lse;                // [T, Hq]
+    const int32_t* q_start;    // [B + 1]
+    const int32_t* kv_len;     // [B]
+    const int32_t* table;      // [B, max_pages]; over the prefix: its pages
+    int64_t table_stride;
+    int32_t B, T, Hq, Hkv, group;
+    int32_t n_pages, page_shift, max_pages;
+    int32_t prefix_len;        // tokens before a sequence's own
+    int32_t over_prefix;       // 1: all rows against the prefix; 0: each sequence against its own tokens
+    int32_t rows_above;        // the pass takes sequences with more rows than this (a sequence's rows are its
+    int32_t rows_upto;         // new tokens * group) and no more than this
+    int32_t window, cols, n_global;  // cols = max(sinks, n_global)
+    float scale_log2;
+    float* part_o;             // [2 * CTAs * R, D] parts of cut items (this pass's)
+    float2* part_ml;           // [2 * CTAs * R] running maximum (log2 units), sum
+    int32_t part_row0;         // index of the first of them in the arrays that join_kernel reads
+    RowInfo* info;             // [T, Hq]
+    float* acc;                // null: finished rows go to o and lse; else [T, Hq, D] unnormalised,
+    float2* acc_ml;            // [T, Hq]
+    int32_t* status;
+    long long timeout;
+    int32_t debug_flags;
+};
+
+enum : int32_t { ST_PAGED_WAIT = 64 };
+
+// One sequence as a pass sees it.
+struct SeqView {
+    int32_t first;  // its first row in the token tensors
+    int32_t m;      // new tokens
+    int32_t len;    // keys
+    int32_t p0;     // position of its first new token, relative to its first key
+};
+
+// Tokens of sequence b in the cache: no more than its table has room for.
+__device__ __forceinline__ int cached_len(const PassParams& p, int b)
+{
+    return min(max(__ldg(&p.kv_len[b]), 0), p.max_pages << p.page_shift);
+}
+
+__device__ __forceinline__ SeqView load_seq(const PassParams& p, int b)
+{
+    SeqView s;
+    if (p.over_prefix) {
+        s.first = 0;
+        s.m = min(max(__ldg(&p.q_start[p.B]), 0), p.T);
+        s.len = p.prefix_len;
+        s.p0 = 0;  // differs from row to row: see PassBounds
+    } else {
+        const int a = min(max(__ldg(&p.q_start[b]), 0), p.T);
+        s.first = a;
+        s.m = max(min(__ldg(&p.q_start[b + 1]), p.T) - a, 0);
+        s.len = cached_len(p, b);
+        s.p0 = s.len - s.m;
+    }
+    return s;
+}
+
+// Does the pass take a sequence of this many rows?
+__device__ __forceinline__ bool takes(const PassParams& p, int rows)
+{
+    return rows > p.rows_above && rows <= p.rows_upto;
+}
+
+// Units of the items whose rows stand at positions pa .. pb (counted like the keys
+// they are compared with): `ns` units of sinks from 0 on, then those from `bs` on;
+// nt in all (one, empty, where a row sees nothing: it still has to be written).
+struct Units {
+    int32_t ns, bs, nt, hi;  // keys end before hi
+    __device__ __forceinline__ int key(int i, int UK) const { return (i < ns ? i : bs + (i - ns)) * UK; }
+};
+
+__device__ __forceinline__ Units units_of(const PassParams& p, int pa, int pb, int len, int UK)
+{
+    // positions count the prefix; a sequence's own keys begin behind it
+    const int off = p.over_prefix ? 0 : p.prefix_len;
+    Units u;
+    u.hi = min(max(pb - off + 1, 0), len);
+    const int c = min(max(p.cols - off, 0), u.hi);
+    int lo = u.hi;
+    if (pa < p.n_global)
+        lo = 0;
+    else if (p.window >= 0)  // 64 bits: a row before its sequence's first key stands at a negative position
+        lo = static_cast<int>(min(max(static_cast<int64_t>(pa) - p.window - off, int64_t(0)),
+                                  static_cast<int64_t>(u.hi)));
+    u.ns = (c + UK - 1) / UK;
+    u.bs = max(lo / UK, u.ns);
+    const int be = lo < u.hi ? (u.hi + UK - 1) / UK : u.bs;
+    u.nt = max(u.ns + max(be - u.bs, 0), 1);
+    return u;
+}
+
+// Positions of the first and last row of an item; over the prefix the rows come
+// from many sequences and the bounds hold for all rows of the pass.
+struct PassBounds {
+    int lo, hi;
+};
+
+template <int R, int UK>
+__device__ __forceinline__ Units item_units(const PassParams& p, const PassBounds& pb, const SeqView& s, int rb)
+{
+    if (p.over_prefix) return units_of(p, pb.lo, pb.hi, s.len, UK);
+    const int r0 = rb * R;
+    const int r1 = min(r0 + R, s.m * p.group) - 1;
+    const int base = p.prefix_len + s.p0;
+    return units_of(p, base + r0 / p.group, base + r1 / p.group, s.len, UK);
+}
+
+// Position of a token (prefix included), for a pass over the prefix: the sequence
+// is the last one that starts at or before it.
+__device__ __forceinline__ int token_position(const PassParams& p, int t)
+{
+    int lo = 0, hi = p.B;  // q_start[lo] <= t < q_start[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (__ldg(&p.q_start[mid]) <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int first = __ldg(&p.q_start[lo]), next = __ldg(&p.q_start[lo + 1]);
+    return p.prefix_len + cached_len(p, lo) - (next - first) + (t - first);
+}
+
+// Where a CTA is on the line of units.
+struct Cursor {
+    int b, rb, h;  // item
+    int i;         // unit of the item
+    SeqView s;
+    Units u;
+};
+
+// Move to the first unit of the next item; at the end of the line b reaches n_seq.
+template <int R, int UK>
+__device__ __forceinline__ void next_item(const PassParams& p, const PassBounds& pb, Cursor& c, int n_seq)
+{
+    c.i = 0;
+    if (++c.h < p.Hkv) return;
+    c.h = 0;
+    if (++c.rb * R >= c.s.m * p.group) {
+        c.rb = 0;
+        do {
+            if (++c.b >= n_seq) return;
+            c.s = load_seq(p, c.b);
+        } while (c.s.m == 0 || !takes(p, c.s.m * p.group));
+    }
+    c.u = item_units<R, UK>(p, pb, c.s, c.rb);
+}
+
+// The piece of the line that this CTA takes: [u0, u1) of U units, G CTAs with
+// work.  Called by all NT threads; `sh` holds NT / 32 + 4 int64 in shared memory.
+struct Piece {
+    int64_t U, u0, u1;
+    int G;
+    PassBounds pb;
+    Cursor c;  // at u0 (valid when u0 < u1)
+};
+
+template <int R, int UK>
+__device__ __forceinline__ int64_t seq_units(const PassParams& p, const PassBounds& pb, const SeqView& s)
+{
+    const int rows = s.m * p.group;
+    if (rows == 0 || !takes(p, rows)) return 0;
+    const int nrb = (rows + R - 1) / R;
+    int64_t n = 0;
+    if (p.over_prefix) {
+        n = static_cast<int64_t>(nrb) * item_units<R, UK>(p, pb, s, 0).nt;
+    } else {
+        for (int rb = 0; rb < nrb; rb++) n += item_units<R, UK>(p, pb, s, rb).nt;
+    }
+    return n * p.Hkv;
+}
+
+template <int R, int UK, int NT>
+__device__ __forceinline__ Piece find_piece(const PassParams& p, int min_units, int64_t* sh)
+{
+    constexpr int NWARP = NT / 32;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    Piece r;
+    r.pb = PassBounds{0, 0};
+    const int n_seq = p.over_prefix ? 1 : p.B;
+    if (p.over_prefix) {
+        // the rows' positions: the nearest and the farthest of all sequences
+        int lo = INT32_MAX, hi = INT32_MIN;
+        for (int b = tid; b < p.B; b += NT) {
+            const int m = __ldg(&p.q_start[b + 1]) - __ldg(&p.q_start[b]);
+            if (m <= 0) continue;
+            const int last = p.prefix_len + cached_len(p, b) - 1;
+            lo = min(lo, last - m + 1);
+            hi = max(hi, last);
+        }
+        for (int o = 16; o; o >>= 1) {
+            lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        if (lane == 0) sh[warp] = lo;
+        __syncthreads();
+        for (int w = 0; w < NWARP; w++) lo = min(lo, static_cast<int>(sh[w]));
+        __syncthreads();
+        if (lane == 0) sh[warp] = hi;
+        __syncthreads();
+        for (int w = 0; w < NWARP; w++) hi = max(hi, static_cast<int>(sh[w]));
+        __syncthreads();
+        r.pb = PassBounds{lo, hi};
+    }
+    // units of this thread's sequences, and of those before them
+    const int per = (n_seq + NT - 1) / NT;
+    const int b0 = min(tid * per, n_seq), b1 = min(b0 + per, n_seq);
+    int64_t own = 0;
+    for (int b = b0; b < b1; b++) own += seq_units<R, UK>(p, r.pb, load_seq(p, b));
+    int64_t incl = own;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sh[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - own, U = 0;
+    for (int w = 0; w < NWARP; w++) {
+        if (w < warp) before += sh[w];
+        U += sh[w];
+    }
+    r.U = U;
+    // as many CTAs as get min_units units each
+    int64_t G = (U + min_units - 1) / min_units;
+    G = min(G, static_cast<int64_t>(gridDim.x));
+    r.G = static_cast<int>(G);
+    const int64_t c = blockIdx.x;
+    r.u0 = r.u1 = 0;
+    if (c < G) {
+        r.u0 = c * U / G;
+        r.u1 = (c + 1) * U / G;
+    }
+    int* found = reinterpret_cast<int*>(sh + NWARP);  // b, units before it (2 words)
+    if (r.u0 < r.u1 && before <= r.u0 && r.u0 < before + own) {
+        int64_t at = before;
+        for (int b = b0; b < b1; b++) {
+            const int64_t n = seq_units<R, UK>(p, r.pb, load_seq(p, b));
+            if (r.u0 < at + n) {
+                found[0] = b;
+                sh[NWARP + 1] = at;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    if (r.u0 < r.u1) {
+        r.c.b = found[0];
+        int64_t at = sh[NWARP + 1];
+        r.c.s = load_seq(p, r.c.b);
+        r.c.rb = 0;
+        for (;;) {
+            r.c.u = item_units<R, UK>(p, r.pb, r.c.s, r.c.rb);
+            const int64_t n = static_cast<int64_t>(r.c.u.nt) * p.Hkv;
+            if (r.u0 < at + n) break;
+            at += n;
+            r.c.rb++;
+        }
+        const int rest = static_cast<int>(r.u0 - at);
+        r.c.h = rest / r.c.u.nt;
+        r.c.i = rest % r.c.u.nt;
+    }
+    return r;
+}
+
+// CTA whose piece holds unit u.
+__device__ __forceinline__ int cta_of(const Piece& r, int64_t u)
+{
+    return static_cast<int>(((u + 1) * r.G + r.U - 1) / r.U) - 1;
+}
+
+// Page of key k (k below the sequence's length), or a page past the cache's end
+// (which the tensor map fills with zeros) where the table names none of its pages.
+__device__ __forceinline__ int page_of(const PassParams& p, const Cursor& c, int k)
+{
+    const int pg = __ldg(&p.table[static_cast<int64_t>(c.b) * p.table_stride + (k >> p.page_shift)]);
+    return pg >= 0 && pg < p.n_pages ? pg : p.n_pages;
+}
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3,
+                                            int c4)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_addr(dst)),
+        "l"(tmap), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
+
+// Programmatic dependent launch: the next kernel of the stream may be set up now;
+// wait until the previous one's memory is visible.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// Joining
+// ---------------------------------------------------------------------------
+
+struct JoinParams {
+    const float* part_o;
+    const float2* part_ml;
+    const RowInfo* info[2];   // the passes' (the second null without a prefix)
+    const float* acc[2];
+    const float2* acc_ml[2];
+    __nv_bfloat16* o;
+    int64_t o_token, o_head;
+    float* lse;
+    const int32_t* q_start;
+    int32_t B, T, Hq;
+    int32_t part_rows;        // rows of the part arrays
+};
+
+// Rows whose result lies in parts (and, with a prefix, all rows): O = sum of
+// O_k 2^(m_k - M) over sum of l_k 2^(m_k - M), M the largest m_k, in the order of
+// the parts.  WPR warps share a row (each takes every WPR-th part, then they are
+// added in the order of the warps): one where rows are many, eight where a few
+// rows have up to a part per CTA, whose loads are then in flight together.
+template <int D, int WPR, bool PREFIX>
+__global__ void __launch_bounds__(256) join_kernel(const JoinParams p)
+{
+    constexpr int kRows = 8 / WPR;
+    constexpr int E = D / 32;  // elements of a lane
+    wait_previous_kernel();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int sub = warp % WPR;
+    __shared__ float sh_o[8][D];
+    __shared__ float sh_m[8], sh_l[8];
+    const int64_t total = static_cast<int64_t>(min(max(__ldg(&p.q_start[p.B]), 0), p.T)) * p.Hq;
+    // every warp of a block makes the same number of rounds
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < total;
+         row0 += static_cast<int64_t>(gridDim.x) * kRows) {
+        const int64_t row = row0 + warp / WPR;
+        const bool have = row < total;
+        float acc[E];
+#pragma unroll
+        for (int e = 0; e < E; e++) acc[e] = 0.f;
+        float M = -INFINITY, L = 0.f;
+        bool write = PREFIX;
+        auto add = [&](const float* src, float2 ml) {
+            if (ml.x == -INFINITY) return;
+            const float mn = fmaxf(M, ml.x);
+            const float a = ex2_approx(M - mn), b = ex2_approx(ml.x - mn);
+#pragma unroll
+            for (int e = 0; e < E; e++) acc[e] = acc[e] * a + src[e] * b;
+            L = L * a + ml.y * b;
+            M = mn;
+        };
+        if (have) {
+#pragma unroll
+            for (int s = 0; s < (PREFIX ? 2 : 1); s++) {
+                RowInfo ri = p.info[s][row];
+                // a row that no sequence covers (q_start not ascending from 0) has no entry: nothing of it
+                // is followed
+                if (ri.n < 0 || ri.n > p.part_rows || ri.stride < 0 || ri.stride > p.part_rows || ri.first < 0 ||
+                    ri.second < 0 ||
+                    (ri.n > 0 && (ri.first >= p.part_rows ||
+                                  ri.second + static_cast<int64_t>(ri.n - 2) * ri.stride >= p.part_rows)))
+                    continue;
+                if (ri.n == 0) {
+                    if (PREFIX && sub == 0) {
+                        float v[E];
+#pragma unroll
+                        for (int e = 0; e < E; e++) v[e] = p.acc[s][row * D + lane * E + e];
+                        add(v, p.acc_ml[s][row]);
+                    }
+                    continue;
+                }
+                write = true;
+                constexpr int K = 4;  // parts in flight
+                for (int k0 = sub; k0 < ri.n; k0 += K * WPR) {
+                    float v[K][E];
+                    float2 ml[K];
+#pragma unroll
+                    for (int j = 0; j < K; j++) {
+                        const int k = k0 + j * WPR;
+                        ml[j] = make_float2(-INFINITY, 0.f);
+                        if (k >= ri.n) continue;
+                        const int64_t at = k == 0 ? ri.first : ri.second + static_cast<int64_t>(k - 1) * ri.stride;
+                        ml[j] = p.part_ml[at];
+#pragma unroll
+                        for (int e = 0; e < E; e++) v[j][e] = p.part_o[at * D + lane * E + e];
+                    }
+#pragma unroll
+                    for (int j = 0; j < K; j++) add(v[j], ml[j]);
+                }
+            }
+        }
+        if constexpr (WPR > 1) {
+#pragma unroll
+            for (int e = 0; e < E; e++) sh_o[warp][lane * E + e] = acc[e];
+            if (lane == 0) {
+                sh_m[warp] = M;
+                sh_l[warp] = L;
+            }
+            __syncthreads();
+            if (sub == 0) {
+                for (int w = 1; w < WPR; w++) {
+                    float v[E];
+#pragma unroll
+                    for (int e = 0; e < E; e++) v[e] = sh_o[warp + w][lane * E + e];
+                    add(v, make_float2(sh_m[warp + w], sh_l[warp + w]));
+                }
+            }
+            __syncthreads();
+        }
+        if (have && write && sub == 0) {
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const int t = static_cast<int>(row / p.Hq), h = static_cast<int>(row % p.Hq);
+            __nv_bfloat16* dst = p.o + t * p.o_token + h * p.o_head + lane * E;
+            if constexpr (E == 4)
+                *reinterpret_cast<uint2*>(dst) =
+                    make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+            else
+                *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+            if (lane == 0) p.lse[row] = L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+        }
+    }
+}
+
+}  // namespace sa
