@@ -10,7 +10,7 @@ CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libsparse_attn.so")
 SOURCES = ["capi.cu", "block_mask.cpp", "fwd_noalloc.cu", "bwd.cu", "cache.cu"]
-HEADERS = ["sm100.cuh", "fwd_sm100.cuh", "bwd_sm100.cuh", "stride_sm100.cuh", "paged_sm100.cuh", "decode_sm100.cuh",
+HEADERS = ["sm100.cuh", "fwd_sm100.cuh", "bwd_sm100.cuh", "stride_sm100.cuh", "paged_sm100.cuh", "decode_sm100.cuh", "chunk_sm100.cuh",
            "rotary_sm100.cuh",
            "tma_host.h", "runtime.h"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "../../include/sparse_attn.h"
+#include "chunk_sm100.cuh"
 #include "decode_sm100.cuh"
 #include "rotary_sm100.cuh"
 #include "runtime.h"
@@ -120,7 +121,7 @@ int batch_status(const sa_cache_batch* b, const sa_kv_cache* c)
     if (b->B == 0 || b->T == 0) return SA_OK;
     if (!b->q_start || !b->kv_len || (b->max_pages > 0 && !b->table)) return SA_ERR_INVALID_ARG;
     if (b->B > 1 && b->table_stride < b->max_pages) return SA_ERR_INVALID_ARG;
-    if (int64_t(b->max_pages) * c->page_size > INT_MAX / 2) return SA_ERR_UNSUPPORTED;  // positions are 32 bits
+    if (int64_t(b->max_pages) * c->page_size > INT_MAX / 4) return SA_ERR_UNSUPPORTED;  // positions are 32 bits
     return SA_OK;
 }
 
@@ -192,7 +193,7 @@ extern "C" int sparse_attn_cache_append(const sa_view* k, const sa_view* v, cons
     if ((q == nullptr) != (q_out == nullptr) || (q && (!rotary || Hq < 0)) || pos_axis_stride < 0 || pos_offset < 0 ||
         (positions && !rotary))
         return SA_ERR_INVALID_ARG;
-    if (pos_offset > INT_MAX / 2) return SA_ERR_UNSUPPORTED;  // a token's position is 32 bits
+    if (pos_offset > INT_MAX / 4) return SA_ERR_UNSUPPORTED;  // a token's position is 32 bits
     const int32_t B = batch->B, T = batch->T, Hkv = cache->n_pages > 0 ? cache->Hkv : 0;
     const int32_t H = q ? Hq : 0;
     if (B == 0 || T == 0 || H + Hkv == 0) return SA_OK;
@@ -245,8 +246,8 @@ constexpr int kDecodeCtas = 2;  // CTAs of decode_kernel on one SM
 // prefix, each pass's finished rows.
 struct CachedLayout {
     size_t part_o, part_ml, info[2], acc[2], acc_ml[2], total;
-    int64_t rows;       // part rows of one pass
-    int64_t part_rows;  // of all passes
+    int64_t rows_decode, rows_chunk;  // part rows of one pass by either kernel
+    int64_t part_rows;                // of all passes
 };
 
 CachedLayout cached_layout(int32_t T, int32_t Hq, int32_t D, bool prefix)
@@ -254,8 +255,10 @@ CachedLayout cached_layout(int32_t T, int32_t Hq, int32_t D, bool prefix)
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     const int n_sm = device_sm_count() > 0 ? device_sm_count() : 148;
     CachedLayout w{};
-    w.rows = 2 * int64_t(kDecodeCtas) * n_sm * 32;
-    w.part_rows = w.rows * (prefix ? 2 : 1);
+    w.rows_decode = 2 * int64_t(kDecodeCtas) * n_sm * 32;
+    w.rows_chunk = 2 * int64_t(n_sm) * 256;
+    // the sequences' own pass may take both kernels, that over the prefix takes one
+    w.part_rows = w.rows_decode + w.rows_chunk + (prefix ? w.rows_chunk : 0);
     const size_t th = size_t(T) * Hq;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -356,32 +359,81 @@ int launch_join(const JoinParams& j, bool prefix, cudaStream_t st)
 }
 
 template <int D>
-int run_paged(const sa_kv_cache& cache, PassParams p, JoinParams j, const CachedLayout& w, uint8_t* ws,
+int launch_chunk(const sa_kv_cache& cache, const PassParams& p, bool overlap, cudaStream_t st)
+{
+    using C = ChunkCfg<D>;
+    auto kern = chunk_kernel<D>;
+    static bool attr_set[kMaxDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SA_ERR_CUDA;
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+            return SA_ERR_CUDA;
+        // the warpgroups' register split must fit what the kernel is launched with
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return SA_ERR_CUDA;
+        if (fa.numRegs * C::kThreads < kRegSplitTotal) return SA_ERR_UNSUPPORTED;
+        attr_set[dev] = true;
+    }
+    CUtensorMap mk, mv;
+    const uint32_t rows = cache.page_size < C::UK ? cache.page_size : C::UK;
+    if (!make_map_pages(&mk, cache.k, cache, rows, 1) || !make_map_pages(&mv, cache.v, cache, rows, 1))
+        return SA_ERR_CUDA;
+    return launch_after(kern, dim3(device_sm_count()), C::kThreads, C::kSmemBytes, st, overlap, mk, mv, p);
+}
+
+// Part arrays and row entries of one pass, from part row `row0` on.
+void use_parts(PassParams& p, const CachedLayout& w, uint8_t* ws, int which, int64_t row0, int D, bool prefix)
+{
+    p.part_row0 = static_cast<int32_t>(row0);
+    p.part_o = reinterpret_cast<float*>(ws + w.part_o) + row0 * D;
+    p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml) + row0;
+    p.info = reinterpret_cast<RowInfo*>(ws + w.info[which]);
+    p.acc = prefix ? reinterpret_cast<float*>(ws + w.acc[which]) : nullptr;
+    p.acc_ml = prefix ? reinterpret_cast<float2*>(ws + w.acc_ml[which]) : nullptr;
+}
+
+// Most rows of an item of decode_kernel; a sequence with more goes to chunk_kernel,
+// whose 128-row tiles it fills at least a quarter.
+constexpr int kDecodeRows = 32;
+
+template <int D>
+int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const CachedLayout& w, uint8_t* ws,
               const int32_t* prefix_table, int32_t max_q, cudaStream_t st)
 {
     const bool prefix = p.prefix_len > 0;
     p.rows_above = 0;
     p.rows_upto = INT_MAX;
-    auto pass = [&](const PassParams& pp, int64_t rows, bool overlap) {
+    auto decode = [&](const PassParams& pp, int64_t rows, bool overlap) {
         return rows <= 16 ? launch_decode<D, 1>(cache, pp, overlap, st) : launch_decode<D, 2>(cache, pp, overlap, st);
     };
     if (prefix) {
+        // the rows of all sequences against the prefix
         PassParams pp = p;
         pp.over_prefix = 1;
         pp.table = prefix_table;
         pp.table_stride = 0;
-        pp.part_row0 = static_cast<int32_t>(w.rows);
-        pp.part_o = p.part_o + w.rows * D;
-        pp.part_ml = p.part_ml + w.rows;
-        pp.info = reinterpret_cast<RowInfo*>(ws + w.info[1]);
-        pp.acc = reinterpret_cast<float*>(ws + w.acc[1]);
-        pp.acc_ml = reinterpret_cast<float2*>(ws + w.acc_ml[1]);
-        p.acc = reinterpret_cast<float*>(ws + w.acc[0]);
-        p.acc_ml = reinterpret_cast<float2*>(ws + w.acc_ml[0]);
-        if (int rc = pass(pp, int64_t(p.T) * p.group, false)) return rc;
+        use_parts(pp, w, ws, 1, w.rows_decode + w.rows_chunk, D, true);
+        const int64_t rows = int64_t(p.T) * p.group;
+        if (int rc = rows <= kDecodeRows ? decode(pp, rows, false) : launch_chunk<D>(cache, pp, false, st)) return rc;
     }
-    const int64_t rows = int64_t(max_q > 0 ? max_q : (p.T + p.B - 1) / p.B) * p.group;
-    if (int rc = pass(p, rows, prefix)) return rc;
+    // each sequence against its own tokens: by decode_kernel alone where no sequence is known to have
+    // more than its rows (it can take any), by chunk_kernel alone where there is one sequence of many rows,
+    // else by both, each taking the sequences that suit it
+    const int64_t rows = int64_t(max_q > 0 ? max_q : (int64_t(p.T) + p.B - 1) / p.B) * p.group;
+    if (rows <= kDecodeRows || p.B > 1) {
+        PassParams pp = p;
+        int64_t most = rows;
+        if (rows > kDecodeRows) most = pp.rows_upto = p.group <= 16 ? 16 : kDecodeRows;
+        use_parts(pp, w, ws, 0, 0, D, prefix);
+        if (int rc = decode(pp, most, prefix)) return rc;
+        p.rows_above = pp.rows_upto;
+    }
+    if (rows > kDecodeRows) {
+        const bool overlap = prefix || p.B > 1;
+        use_parts(p, w, ws, 0, w.rows_decode, D, prefix);
+        if (int rc = launch_chunk<D>(cache, p, overlap, st)) return rc;
+    }
     return launch_join<D>(j, prefix, st);
 }
 
@@ -397,7 +449,7 @@ int fwd_paged(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* 
     if (!(scale > 0.f) || !std::isfinite(scale)) return SA_ERR_INVALID_ARG;
     if (int rc = check_pattern(*pattern)) return rc;
     if (pattern->causal != 1 || pattern->stride > 0 || pattern->area > 0) return SA_ERR_UNSUPPORTED;
-    if (prefix_len > INT_MAX / 2) return SA_ERR_UNSUPPORTED;
+    if (prefix_len > INT_MAX / 4) return SA_ERR_UNSUPPORTED;
     const int32_t T = batch->T;
     if (batch->B == 0 || T == 0 || Hq == 0) return SA_OK;
     if (cache->Hkv == 0 || cache->n_pages == 0 || Hq % cache->Hkv) return SA_ERR_UNSUPPORTED;
@@ -443,16 +495,13 @@ int fwd_paged(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* 
     p.n_global = clip_to(pattern->n_global, longest);
     p.cols = clip_to(pattern->sinks > pattern->n_global ? pattern->sinks : pattern->n_global, longest);
     p.scale_log2 = scale * 1.44269504088896340736f;
-    p.part_o = reinterpret_cast<float*>(ws + w.part_o);
-    p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
-    p.info = reinterpret_cast<RowInfo*>(ws + w.info[0]);
     p.status = status;
     p.timeout = wait_limit_cycles();
     p.debug_flags = debug_flags();
     JoinParams j{};
-    j.part_o = p.part_o;
-    j.part_ml = p.part_ml;
-    j.info[0] = p.info;
+    j.part_o = reinterpret_cast<const float*>(ws + w.part_o);
+    j.part_ml = reinterpret_cast<const float2*>(ws + w.part_ml);
+    j.info[0] = reinterpret_cast<const RowInfo*>(ws + w.info[0]);
     j.o = p.o;
     j.o_token = p.o_token;
     j.o_head = p.o_head;
