@@ -58,34 +58,66 @@ def _declare() -> None:
 _declare()
 
 
-def _bf16_rows(where: str, name: str, t, dims: int, device=None) -> None:
-    """A bf16 CUDA tensor of `dims` dimensions whose rows are contiguous."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != dims or t.stride(-1) != 1:
+# Calls of a few microseconds on the device are common here (one decoding step), so what a call does on
+# the host is kept short: attributes are read once, and the device is only switched when it has to be.
+
+_BF16, _I32 = torch.bfloat16, torch.int32
+_ref = ctypes.byref
+
+
+def _rows(where: str, name: str, t, dims: int, device=None):
+    """(shape, strides) of a bf16 CUDA tensor of `dims` dimensions with contiguous rows."""
+    st = t.stride()
+    if t.dtype is not _BF16 or not t.is_cuda or len(st) != dims or st[-1] != 1:
         raise TypeError(f"{where}: {name} must be a {dims}-dimensional bf16 CUDA tensor with contiguous rows")
     if device is not None and t.device != device:
         raise TypeError(f"{where}: {name} is on {t.device}, not on {device}")
+    return t.shape, st
 
 
 def _int32(where: str, name: str, t, dims: int, device) -> None:
-    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    if t.dtype is not _I32 or not t.is_cuda or t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
         raise TypeError(f"{where}: {name} must be a {dims}-dimensional int32 CUDA tensor with contiguous rows")
     if t.device != device:
         raise TypeError(f"{where}: {name} is on {t.device}, not on {device}")
 
 
-def _same_shape(where: str, name: str, t, shape) -> None:
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{where}: {name} has the shape {tuple(t.shape)}, not {tuple(shape)}")
+def _mismatch(where: str, name: str, shape, want):
+    raise ValueError(f"{where}: {name} has the shape {tuple(shape)}, not {tuple(want)}")
 
 
-def _tokens(t) -> _View:
+def _tokens(t, st=None) -> _View:
     """View of a tensor of tokens [T, H, D]."""
-    return _View(t.data_ptr(), 0, t.stride(1), t.stride(0))
+    st = st or t.stride()
+    return _View(t.data_ptr(), 0, st[1], st[0])
 
 
-def _sequences(t) -> _View:
+def _sequences(t, st=None) -> _View:
     """View of whole sequences [B, H, N, D]."""
-    return _View(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    st = st or t.stride()
+    return _View(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _call(fn, where: str, device, stream, *args) -> None:
+    """Call fn(*args, stream handle) with `device` current."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream_handle(stream, device))
+    if status:
+        _check(status, where)
+
+
+def _raw_stream(index: int) -> int:
+    """Handle of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+if not hasattr(torch._C, "_cuda_getCurrentRawStream"):  # a torch without CUDA, or without the short way
+    def _raw_stream(index: int) -> int:  # noqa: F811
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 class Rotary:
@@ -106,6 +138,7 @@ class Rotary:
         self._axis = (ctypes.c_int32 * max(len(axis), 1))(*axis) if axis is not None else None
         self._struct = _Rotary(len(freq), self.n_axes, int(self.interleaved), ctypes.addressof(self._freq),
                                ctypes.addressof(self._axis) if axis is not None else None)
+        self._ref = _ref(self._struct)
 
 
 class KVCache:
@@ -113,19 +146,16 @@ class KVCache:
     strides (any order of heads and places in memory; rows of D contiguous)."""
 
     def __init__(self, k_pages, v_pages):
-        _bf16_rows("KVCache", "k_pages", k_pages, 4)
-        _bf16_rows("KVCache", "v_pages", v_pages, 4, k_pages.device)
+        _rows("KVCache", "k_pages", k_pages, 4)
+        _rows("KVCache", "v_pages", v_pages, 4, k_pages.device)
         if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
             raise ValueError("KVCache: k_pages and v_pages differ in shape or strides")
-        self.k, self.v = k_pages, v_pages
+        self.k, self.v, self.device = k_pages, v_pages, k_pages.device
         n, self.Hkv, self.page_size, self.D = k_pages.shape
         st = k_pages.stride()
         self._struct = _KVCache(k_pages.data_ptr(), v_pages.data_ptr(), n, self.page_size, self.Hkv, self.D, st[0],
                                 st[1], st[2])
-
-    @property
-    def device(self):
-        return self.k.device
+        self._ref = _ref(self._struct)
 
 
 class CacheBatch:
@@ -143,51 +173,55 @@ class CacheBatch:
         B = kv_len.shape[0]
         if q_start.shape[0] != B + 1 or table.shape[0] != B:
             raise ValueError("CacheBatch: q_start [B + 1], kv_len [B] and table [B, max_pages] disagree on B")
-        self.q_start, self.kv_len, self.table, self.max_q = q_start, kv_len, table, max_q
+        self.q_start, self.kv_len, self.table, self.max_q, self.device = q_start, kv_len, table, max_q, dev
         self._struct = _CacheBatch(B, 0, max_q or 0, table.shape[1], table.stride(0) if B > 1 else table.shape[1],
                                    q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr())
 
-    @property
-    def device(self):
-        return self.q_start.device
-
     def _c(self, T: int) -> _CacheBatch:
-        s = self._struct
-        return _CacheBatch(s.B, T, s.max_q, s.max_pages, s.table_stride, s.q_start, s.kv_len, s.table)
+        s = _CacheBatch.from_buffer_copy(self._struct)
+        s.T = T
+        return s
 
 
 def _rotate(where, q, k, positions, spec, backward, q_out, k_out, stream):
-    _bf16_rows(where, "q", q, 4)
-    B, Hq, N, D = q.shape
+    shape, st = _rows(where, "q", q, 4)
+    B, Hq, N, D = shape
     dev = q.device
     _int32(where, "positions", positions, 3, dev)
-    if tuple(positions.shape) not in ((spec.n_axes, B, N), (spec.n_axes, 1, N)):
+    n_axes, Bp, Np = positions.shape
+    if n_axes != spec.n_axes or (Bp != B and Bp != 1) or Np != N:
         raise ValueError(f"{where}: positions must be [{spec.n_axes}, {B} or 1, {N}]")
-    pairs = [("q", q, q_out)]
+    qv = _sequences(q, st)
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=_BF16, device=dev)
+        ov = _sequences(q_out)
+    else:
+        oshape, ost = _rows(where, "q_out", q_out, 4, dev)
+        if oshape != shape:
+            _mismatch(where, "q_out", oshape, shape)
+        ov = _sequences(q_out, ost)
+    kv = okv = None
+    Hkv = 0
     if k is not None:
-        _bf16_rows(where, "k", k, 4, dev)
-        _same_shape(where, "k", k, (B, k.shape[1], N, D))
-        pairs.append(("k", k, k_out))
+        kshape, kst = _rows(where, "k", k, 4, dev)
+        Hkv = kshape[1]
+        if kshape[0] != B or kshape[2] != N or kshape[3] != D:
+            _mismatch(where, "k", kshape, (B, Hkv, N, D))
+        if k_out is None:
+            k_out = torch.empty(kshape, dtype=_BF16, device=dev)
+            okv = _ref(_sequences(k_out))
+        else:
+            oshape, ost = _rows(where, "k_out", k_out, 4, dev)
+            if oshape != kshape:
+                _mismatch(where, "k_out", oshape, kshape)
+            okv = _ref(_sequences(k_out, ost))
+        kv = _ref(_sequences(k, kst))
     elif k_out is not None:
         raise ValueError(f"{where}: k_out without k")
-    outs, views = [], []
-    for name, x, out in pairs:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        else:
-            _bf16_rows(where, name + "_out", out, 4, dev)
-            _same_shape(where, name + "_out", out, x.shape)
-        outs.append(out)
-        views.append((_sequences(x), _sequences(out)))
-    shape = _Shape(B, Hq, k.shape[1] if k is not None else 0, N, D)
-    ref = ctypes.byref
-    kv = (ref(views[1][0]), ref(views[1][1])) if k is not None else (None, None)
-    with torch.cuda.device(dev):
-        st = _stream_handle(stream, dev)
-        _check(lib.sparse_attn_rotary(ref(views[0][0]), kv[0], positions.data_ptr(), positions.stride(0),
-                                      positions.stride(1) if positions.shape[1] > 1 else 0, ref(spec._struct),
-                                      ref(shape), backward, ref(views[0][1]), kv[1], st), "sparse_attn_rotary")
-    return outs[0], (outs[1] if k is not None else None)
+    pst = positions.stride()
+    _call(lib.sparse_attn_rotary, "sparse_attn_rotary", dev, stream, _ref(qv), kv, positions.data_ptr(), pst[0],
+          pst[1] if Bp > 1 else 0, spec._ref, _ref(_Shape(B, Hq, Hkv, N, D)), backward, _ref(ov), okv)
+    return q_out, k_out
 
 
 def rotary(q, k, positions, spec: Rotary, q_out=None, k_out=None, stream=None):
@@ -211,10 +245,13 @@ def cache_append(k, v, cache: KVCache, batch: CacheBatch, rotary: Rotary | None 
     the tokens' positions in the cache (+ ``pos_offset``).  Asynchronous on ``stream``."""
     where = "cache_append"
     dev = cache.device
-    T = k.shape[0]
-    for name, x in (("k", k), ("v", v)):
-        _bf16_rows(where, name, x, 3, dev)
-        _same_shape(where, name, x, (T, cache.Hkv, cache.D))
+    shape, kst = _rows(where, "k", k, 3, dev)
+    T = shape[0]
+    if shape[1] != cache.Hkv or shape[2] != cache.D:
+        _mismatch(where, "k", shape, (T, cache.Hkv, cache.D))
+    vshape, vst = _rows(where, "v", v, 3, dev)
+    if vshape != shape:
+        _mismatch(where, "v", vshape, shape)
     if batch.device != dev:
         raise TypeError(f"{where}: batch is on {batch.device}, not on {dev}")
     pos_ptr, pos_stride = None, 0
@@ -222,30 +259,32 @@ def cache_append(k, v, cache: KVCache, batch: CacheBatch, rotary: Rotary | None 
         if rotary is None:
             raise ValueError(f"{where}: positions without rotary")
         _int32(where, "positions", positions, 2, dev)
-        _same_shape(where, "positions", positions, (rotary.n_axes, T))
+        if tuple(positions.shape) != (rotary.n_axes, T):
+            _mismatch(where, "positions", positions.shape, (rotary.n_axes, T))
         pos_ptr, pos_stride = positions.data_ptr(), positions.stride(0)
     qv = ov = None
     Hq = 0
     if q is not None:
         if rotary is None:
             raise ValueError(f"{where}: q without rotary")
-        _bf16_rows(where, "q", q, 3, dev)
-        Hq = q.shape[1]
-        _same_shape(where, "q", q, (T, Hq, cache.D))
+        qshape, qst = _rows(where, "q", q, 3, dev)
+        Hq = qshape[1]
+        if qshape[0] != T or qshape[2] != cache.D:
+            _mismatch(where, "q", qshape, (T, Hq, cache.D))
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = torch.empty(qshape, dtype=_BF16, device=dev)
+            ov = _ref(_tokens(q_out))
         else:
-            _bf16_rows(where, "q_out", q_out, 3, dev)
-            _same_shape(where, "q_out", q_out, q.shape)
-        qv, ov = ctypes.byref(_tokens(q)), ctypes.byref(_tokens(q_out))
+            oshape, ost = _rows(where, "q_out", q_out, 3, dev)
+            if oshape != qshape:
+                _mismatch(where, "q_out", oshape, qshape)
+            ov = _ref(_tokens(q_out, ost))
+        qv = _ref(_tokens(q, qst))
     elif q_out is not None:
         raise ValueError(f"{where}: q_out without q")
-    ref = ctypes.byref
-    with torch.cuda.device(dev):
-        st = _stream_handle(stream, dev)
-        _check(lib.sparse_attn_cache_append(ref(_tokens(k)), ref(_tokens(v)), ref(cache._struct), ref(batch._c(T)),
-                                            ref(rotary._struct) if rotary is not None else None, pos_ptr, pos_stride,
-                                            int(pos_offset), qv, ov, Hq, st), "sparse_attn_cache_append")
+    _call(lib.sparse_attn_cache_append, "sparse_attn_cache_append", dev, stream, _ref(_tokens(k, kst)),
+          _ref(_tokens(v, vst)), cache._ref, _ref(batch._c(T)), rotary._ref if rotary is not None else None, pos_ptr,
+          pos_stride, int(pos_offset), qv, ov, Hq)
     return q_out
 
 
@@ -266,34 +305,34 @@ def fwd_shared_workspace_bytes(T: int, Hq: int, Hkv: int, D: int) -> int:
 def _attend(fn, q, cache, batch, prefix, pattern, scale, out, lse, workspace, stream):
     where = fn[len("sparse_attn_"):]
     dev = cache.device
-    _bf16_rows(where, "q", q, 3, dev)
-    T, Hq, D = q.shape
-    _same_shape(where, "q", q, (T, Hq, cache.D))
+    shape, st = _rows(where, "q", q, 3, dev)
+    T, Hq, D = shape
+    if D != cache.D:
+        _mismatch(where, "q", shape, (T, Hq, cache.D))
     if batch.device != dev:
         raise TypeError(f"{where}: batch is on {batch.device}, not on {dev}")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = torch.empty(shape, dtype=_BF16, device=dev)
+        ov = _tokens(out)
     else:
-        _bf16_rows(where, "out", out, 3, dev)
-        _same_shape(where, "out", out, q.shape)
+        oshape, ost = _rows(where, "out", out, 3, dev)
+        if oshape != shape:
+            _mismatch(where, "out", oshape, shape)
+        ov = _tokens(out, ost)
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-    elif lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous() or tuple(lse.shape) != (T, Hq):
+    elif lse.dtype is not torch.float32 or lse.device != dev or not lse.is_contiguous() or lse.shape != (T, Hq):
         raise TypeError(f"{where}: lse must be a contiguous fp32 tensor [T, Hq] on {dev}")
-    with torch.cuda.device(dev):
-        st = _stream_handle(stream, dev)
-        if workspace is None:
-            # taken on the stream that uses it, so that it is not handed out again before the kernels are done
-            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
-                workspace = torch.empty(max(_workspace(fn + "_workspace", T, Hq, cache.Hkv, D), 1),
-                                        dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise TypeError(f"{where}: workspace must be a contiguous tensor on {dev}")
-        ref = ctypes.byref
-        _check(getattr(lib, fn)(ref(_tokens(q)), ref(cache._struct), ref(batch._c(T)), *prefix, ref(pattern._c()), Hq,
-                                float(scale if scale is not None else 1.0 / math.sqrt(D)), ref(_tokens(out)),
-                                lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                st), fn)
+    if workspace is None:
+        # taken on the stream that uses it, so that it is not handed out again before the kernels are done
+        need = max(_workspace(fn + "_workspace", T, Hq, cache.Hkv, D), 1)
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise TypeError(f"{where}: workspace must be a contiguous tensor on {dev}")
+    _call(getattr(lib, fn), fn, dev, stream, _ref(_tokens(q, st)), cache._ref, _ref(batch._c(T)), *prefix,
+          _ref(pattern._c()), Hq, scale if scale is not None else 1.0 / math.sqrt(D), _ref(ov), lse.data_ptr(),
+          workspace.data_ptr(), workspace.nbytes)
     return out, lse
 
 
