@@ -62,7 +62,10 @@ RotSpec rot_spec(const sa_rotary* r)
     if (!r) return s;
     s.n_pairs = r->n_pairs;
     for (int i = 0; i < r->n_pairs; i++) {
-        s.turns[i] = r->freq[i] * 0.15915494309189533576888376337251;  // 1 / 2 pi
+        // freq / 2 pi modulo 1 as a 64-bit fraction (whole turns drop out: positions are whole numbers)
+        const long double turns = static_cast<long double>(r->freq[i]) / 6.283185307179586476925286766559005768L;
+        const long double frac = turns - floorl(turns);
+        s.turns[i] = frac >= 1.0L ? 0 : static_cast<uint64_t>(frac * 18446744073709551616.0L);
         s.axis[i] = static_cast<uint8_t>(r->axis ? r->axis[i] : 0);
     }
     return s;
@@ -71,28 +74,29 @@ RotSpec rot_spec(const sa_rotary* r)
 template <int D, bool PAGED>
 int rot_launch(const RotSpec& spec, const RotParams& p, bool inter, cudaStream_t st)
 {
-    const int V = inter || spec.n_pairs % 8 == 0 ? 8 : spec.n_pairs % 2 == 0 ? 2 : 1;
-    const int64_t blocks = (p.rows * (D / (2 * V)) + kRotThreads - 1) / kRotThreads;
+    const RotLayout layout = inter ? kInterleaved : spec.n_pairs % 8 == 0 ? kHalves : kShuffled;
+    const int64_t blocks = (p.rows * (D / (layout == kShuffled ? 4 : 16)) + kRotThreads - 1) / kRotThreads;
     if (blocks > INT_MAX) return SA_ERR_UNSUPPORTED;
     const int heads = p.Hq + p.Hk + p.Hv;
     RotParams pp = p;
-    // heads of one thread: as many as leave each SM eight blocks, so that the sines are taken few
-    // times, and no fewer than one batch of loads
-    const int64_t want = 8 * int64_t(device_sm_count());
-    const int64_t parts = blocks >= want ? 1 : (want + blocks - 1) / blocks;
+    // Heads of one thread.  Few tokens: as many parts as the SMs hold blocks, so that all have work.  Many:
+    // parts that make three rounds of blocks, whose ends then even out, but no fewer than 16 heads, over
+    // which the sines are shared.  16 + 16 heads of 128 at 8192 tokens (512 blocks of the 888 held at once):
+    // one part 24.6 us, parts of 16 26.8, of 4 31.6; 64 + 8 heads of 64 at 2 x 16384 (1024 blocks): one part
+    // 109 us, parts of 24 99, of 4 111.
+    const int64_t held = int64_t(rot_blocks(layout)) * device_sm_count();
+    const bool few = 3 * blocks <= 2 * held;
+    const int64_t parts = few ? held / blocks : (3 * held + blocks - 1) / blocks;
     int64_t per = (heads + parts - 1) / parts;
-    per = (per + kRotUnroll - 1) / kRotUnroll * kRotUnroll;
+    if (!few && per < 16) per = 16;
+    per = (per + 3) / 4 * 4;
     pp.heads_per = static_cast<int32_t>(per);
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + per - 1) / per));
     if (grid.y > 65535) return SA_ERR_UNSUPPORTED;
-    if (inter)
-        rotary_kernel<D, 8, true, PAGED><<<grid, kRotThreads, 0, st>>>(spec, pp);
-    else if (V == 8)
-        rotary_kernel<D, 8, false, PAGED><<<grid, kRotThreads, 0, st>>>(spec, pp);
-    else if (V == 2)
-        rotary_kernel<D, 2, false, PAGED><<<grid, kRotThreads, 0, st>>>(spec, pp);
-    else
-        rotary_kernel<D, 1, false, PAGED><<<grid, kRotThreads, 0, st>>>(spec, pp);
+    auto kern = layout == kInterleaved ? rotary_kernel<D, kInterleaved, PAGED>
+                : layout == kHalves    ? rotary_kernel<D, kHalves, PAGED>
+                                       : rotary_kernel<D, kShuffled, PAGED>;
+    kern<<<grid, kRotThreads, 0, st>>>(spec, pp);
     return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 

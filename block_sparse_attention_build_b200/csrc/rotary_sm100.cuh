@@ -9,9 +9,9 @@
 // them in registers and walks the heads with nothing but wide loads, the
 // rotation and wide stores.  No shared memory, no barrier.
 //
-// The angle is a 64-bit product in turns (positions times freq / 2 pi), reduced
-// to [-1/2, 1/2] before it is rounded to 32 bits: at position 10^6 a 32-bit
-// product would be off by 0.03 radians.
+// The angle counts in turns, as a 64-bit fraction: position times fraction wraps
+// around at a whole turn by itself and is exact (a 32-bit product would be off by
+// 0.03 radians at position 10^6), and its upper 32 bits go to sincospif.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,7 +25,7 @@ constexpr int kMaxPairs = 64;  // D / 2
 constexpr int kMaxAxes = 4;
 
 struct RotSpec {
-    double turns[kMaxPairs];  // freq / 2 pi
+    uint64_t turns[kMaxPairs];  // turns per position, modulo 1: a fraction of 64 bits
     uint8_t axis[kMaxPairs];
     int32_t n_pairs;
 };
@@ -54,99 +54,128 @@ struct RotParams {
     const int32_t* table;
 };
 
-// One access of V bf16 elements.
-template <int V>
-struct Chunk;
-template <>
-struct Chunk<8> {
-    uint4 w;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = w; }
-    __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
-    __device__ __forceinline__ void set_word(int i, uint32_t x)
-    {
-        if (i == 0) w.x = x;
-        else if (i == 1) w.y = x;
-        else if (i == 2) w.z = x;
-        else w.w = x;
-    }
-};
-template <>
-struct Chunk<2> {
-    uint32_t w;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint32_t*>(p); }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint32_t*>(p) = w; }
-    __device__ __forceinline__ uint32_t word(int) const { return w; }
-    __device__ __forceinline__ void set_word(int, uint32_t x) { w = x; }
-};
-template <>
-struct Chunk<1> {
-    uint32_t w;  // the low half holds the element
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint16_t*>(p); }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const
-    {
-        *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w);
-    }
-    __device__ __forceinline__ uint32_t word(int) const { return w; }
-    __device__ __forceinline__ void set_word(int, uint32_t x) { w = x; }
-};
-
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Rotate one thread's part of a row in place.  Halves layout: a and b hold the V
-// elements x and x + n_pairs of V pairs.  Interleaved (V = 8): a and b are
-// neighbouring chunks of four pairs each, and `n` counts the pairs that turn.
-template <int V, bool INTER>
-__device__ __forceinline__ void rotate_chunks(Chunk<V>& a, Chunk<V>& b, const float (&cs)[8], const float (&sn)[8],
-                                              int n)
+// x c + y s of a word's two elements, rounded once to bf16.
+__device__ __forceinline__ uint32_t turn_word(uint32_t x, uint32_t y, float c0, float c1, float s0, float s1)
 {
-    if constexpr (INTER) {
+    return pack_bf16x2(bf_lo(x) * c0 + bf_lo(y) * s0, bf_hi(x) * c1 + bf_hi(y) * s1);
+}
+
+// How a thread holds its part of a row:
+//   kHalves      (j, j + n_pairs), n_pairs a multiple of 8: two chunks of 16 bytes, n_pairs apart,
+//                of 8 pairs
+//   kInterleaved (2j, 2j + 1): two neighbouring chunks of 4 pairs each
+//   kShuffled    (j, j + n_pairs), any n_pairs: one chunk of 8 bytes, whose partners lie in other
+//                lanes' chunks at any offset
+enum RotLayout { kHalves, kInterleaved, kShuffled };
+
+template <int W>
+struct Words {  // one access of W words
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p)
+    {
+        if constexpr (W == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(p);
+            w[0] = x.x;
+            w[1] = x.y;
+            w[2] = x.z;
+            w[3] = x.w;
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
+            w[0] = x.x;
+            w[1] = x.y;
+        }
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const
+    {
+        if constexpr (W == 4)
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    }
+};
+
+// Turn a kShuffled chunk: words 2 l, 2 l + 1 of a row that L lanes hold.  `cs`, `sn`
+// belong to the chunk's four elements (sn with the sign that the element's place in
+// its pair wants): x cos + partner sn.
+template <int L>
+__device__ __forceinline__ void turn_shuffled(Words<2>& x, int P, int lane, const float (&cs)[8], const float (&sn)[8])
+{
+    const int base = lane & ~(L - 1), l = lane & (L - 1);
+    const int S = P >> 1;
+    if ((P & 1) == 0) {
+        // The partner of word w is word w + S in the first half, w - S in the second: register (i + S) mod 2
+        // of some lane either way, so one shuffle per word serves both halves.
+        const bool swap = S & 1;
+        const uint32_t r0 = swap ? x.w[1] : x.w[0], r1 = swap ? x.w[0] : x.w[1];
+        uint32_t y[2];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            Chunk<V>& c = i < 4 ? a : b;
-            const uint32_t w = c.word(i & 3);
-            const float x = bf_lo(w), y = bf_hi(w);
-            const uint32_t r = pack_bf16x2(x * cs[i] - y * sn[i], y * cs[i] + x * sn[i]);
-            c.set_word(i & 3, i < n ? r : w);
+        for (int i = 0; i < 2; i++) {
+            const int w = 2 * l + i;
+            const int src = w < S ? w + S : w - S;
+            y[i] = __shfl_sync(0xffffffffu, i ? r1 : r0, base + ((src >> 1) & (L - 1)));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const uint32_t r = turn_word(x.w[i], y[i], cs[2 * i], cs[2 * i + 1], sn[2 * i], sn[2 * i + 1]);
+            x.w[i] = 2 * l + i < P ? r : x.w[i];
         }
     } else {
-        constexpr int W = V == 8 ? 4 : 1;
+        // partners straddle words: elements e + P begin in the high half of word w + S, e - P in the high half of
+        // word w - S - 1
+        const uint32_t x0 = x.w[0], x1 = x.w[1];
+        auto word = [&](int w) {  // of the row; both registers are offered, the asker picks
+            const int src = base + ((w >> 1) & (L - 1));
+            const uint32_t a = __shfl_sync(0xffffffffu, x0, src), b = __shfl_sync(0xffffffffu, x1, src);
+            return w & 1 ? b : a;
+        };
 #pragma unroll
-        for (int i = 0; i < W; i++) {
-            const uint32_t wa = a.word(i), wb = b.word(i);
-            const float x0 = bf_lo(wa), y0 = bf_lo(wb);
-            const int j = 2 * i;
-            float a1 = 0.f, b1 = 0.f;
-            if constexpr (V > 1) {
-                const float x1 = bf_hi(wa), y1 = bf_hi(wb);
-                a1 = x1 * cs[j + 1] - y1 * sn[j + 1];
-                b1 = y1 * cs[j + 1] + x1 * sn[j + 1];
-            }
-            a.set_word(i, pack_bf16x2(x0 * cs[j] - y0 * sn[j], a1));
-            b.set_word(i, pack_bf16x2(y0 * cs[j] + x0 * sn[j], b1));
+        for (int i = 0; i < 2; i++) {
+            const int w = 2 * l + i, e = 2 * w;
+            const uint32_t up = __funnelshift_r(word(w + S), word(w + S + 1), 16);
+            const uint32_t dn = __funnelshift_r(word(w - S - 1), word(w - S), 16);
+            const uint32_t v = i ? x1 : x0;
+            const uint32_t y = __byte_perm(e < P ? up : dn, e + 1 < P ? up : dn, 0x7610);
+            const uint32_t r = turn_word(v, y, cs[2 * i], cs[2 * i + 1], sn[2 * i], sn[2 * i + 1]);
+            x.w[i] = w < P ? r : v;
         }
     }
 }
 
 constexpr int kRotThreads = 128;
-constexpr int kRotUnroll = 4;  // heads whose loads one thread has in flight
+// Heads whose loads one thread has in flight, and blocks of an SM (which bound the registers), both
+// swept on 16 + 16 heads of 128 at 8192 tokens and 64 + 8 heads of 64 at 2 x 16384: 4 heads of 32 bytes
+// with 6 blocks, 8 of 8 bytes with 8.
+__host__ __device__ constexpr int rot_unroll(RotLayout l) { return l == kShuffled ? 8 : 4; }
+__host__ __device__ constexpr int rot_blocks(RotLayout l) { return l == kShuffled ? 8 : 6; }
 
-// V: elements of one access (8 when the halves start on 16 bytes or pairs are
-// interleaved, else 2 for an even and 1 for an odd number of pairs); the row of D
-// elements is D / (2 V) items of two accesses each.
-template <int D, int V, bool INTER, bool PAGED>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotSpec spec,
+template <int D, RotLayout LAYOUT, bool PAGED>
+__global__ void __launch_bounds__(kRotThreads, rot_blocks(LAYOUT)) rotary_kernel(const __grid_constant__ RotSpec spec,
                                                              const __grid_constant__ RotParams p)
 {
-    constexpr int kItems = D / (2 * V);                     // threads of one token
-    constexpr int kTok = kItems >= 32 ? 1 : 32 / kItems;    // tokens of one warp
+    constexpr int kChunks = LAYOUT == kShuffled ? 1 : 2;    // of one thread
+    constexpr int W = LAYOUT == kShuffled ? 2 : 4;          // words of a chunk
+    constexpr int kItems = D / (2 * W * kChunks);           // threads of one token
+    constexpr int kTok = 32 / kItems;                       // tokens of one warp
     const int64_t gid = static_cast<int64_t>(blockIdx.x) * kRotThreads + threadIdx.x;
     const int64_t t = gid / kItems;
     const int item = static_cast<int>(gid % kItems);
     const int lane = threadIdx.x % 32;
 
+    // The pairs' turns and axes, from parameters to shared memory: a warp's lanes index them apart, which
+    // constant memory would serve one lane at a time (64 + 8 heads of 64, 30 pairs: 133 us so).
+    __shared__ uint64_t sh_turns[kMaxPairs];
+    __shared__ uint8_t sh_axis[kMaxPairs];
+    for (int i = threadIdx.x; i < spec.n_pairs; i += kRotThreads) {
+        sh_turns[i] = spec.turns[i];
+        sh_axis[i] = spec.axis[i];
+    }
+    __syncthreads();
+
     // where the token stands, and where its key and value go
+    bool have;  // lanes without a token stay: others may shuffle with them
     int64_t b = 0, n = 0;
     int64_t page_off = -1;
     int place = 0;
@@ -163,100 +192,149 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
                 if (k == mine) cnt += m;
             }
         }
-        if (t >= p.rows || cnt == 0 || t >= __ldg(&p.q_start[p.B])) return;
-        b = cnt - 1;
+        have = t < p.rows && cnt > 0 && t < __ldg(&p.q_start[p.B]);
+        b = max(cnt - 1, 0);
         const int first = __ldg(&p.q_start[b]), next = __ldg(&p.q_start[b + 1]);
         n = t;
         place = __ldg(&p.kv_len[b]) - (next - first) + static_cast<int>(t - first);
         const int pi = place >> p.page_shift;
-        if (place >= 0 && pi < p.max_pages) {
+        if (have && place >= 0 && pi < p.max_pages) {
             const int page = __ldg(&p.table[b * p.table_stride + pi]);
             if (page >= 0 && page < p.n_pages)
                 page_off = page * p.ko.batch + (place & ((1 << p.page_shift) - 1)) * p.ko.token;
         }
     } else {
-        if (t >= p.rows) return;
+        have = t < p.rows;
         b = t / p.N;
         n = t % p.N;
     }
 
-    // this item's two accesses and the pairs they hold
+    // this thread's chunks and the pair of each of its 8 elements or pairs (-1: stays as it is)
     const int P = spec.n_pairs;
-    int off_a, off_b, n_rot, pair0;
-    if constexpr (INTER) {
-        off_a = 2 * V * item;
-        off_b = off_a + V;
-        pair0 = V * item;
+    int off_a, off_b = 0, pair0 = 0, n_rot = 0;
+    if constexpr (LAYOUT == kInterleaved) {
+        off_a = 16 * item;
+        off_b = off_a + 8;
+        pair0 = 8 * item;
         n_rot = min(max(P - pair0, 0), 8);
-    } else {
-        const int turning = P / V;
+    } else if constexpr (LAYOUT == kHalves) {
+        const int turning = P / 8;
         if (item < turning) {
-            off_a = V * item;
+            off_a = 8 * item;
             off_b = P + off_a;
             pair0 = off_a;
-            n_rot = V;
+            n_rot = 8;
         } else {
-            off_a = 2 * P + 2 * V * (item - turning);
-            off_b = off_a + V;
-            pair0 = 0;
-            n_rot = 0;
+            off_a = 2 * P + 16 * (item - turning);
+            off_b = off_a + 8;
         }
+    } else {
+        off_a = 4 * item;
     }
     float cs[8], sn[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) {
+        int j = i < n_rot ? pair0 + i : -1;
+        float sign = p.sign;
+        if constexpr (LAYOUT == kShuffled) {  // an element is x cos + partner sn: minus in the first of a pair
+            const int e = off_a + i;
+            j = i >= 2 * W ? -1 : e < P ? e : e < 2 * P ? e - P : -1;
+            if (e < P) sign = -sign;
+        }
         cs[i] = 1.f;
         sn[i] = 0.f;
-        if (i < V && i < n_rot) {
-            const int j = pair0 + i;
-            const int ax = spec.axis[j];
+        if (j >= 0 && have) {
             int pos;
             if (PAGED && p.pos == nullptr)
                 pos = place + p.pos_offset;
             else
-                pos = __ldg(&p.pos[ax * p.pos_axis + (PAGED ? t : b * p.pos_batch + n)]);
-            const double turns = static_cast<double>(pos) * spec.turns[j];
-            sincospif(2.f * static_cast<float>(turns - rint(turns)), &sn[i], &cs[i]);
-            sn[i] *= p.sign;
+                pos = __ldg(&p.pos[sh_axis[j] * p.pos_axis + (PAGED ? t : b * p.pos_batch + n)]);
+            // the angle modulo a turn: the low 64 bits of the product, of which the upper 32 are kept
+            const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos)) * sh_turns[j];
+            sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn[i], &cs[i]);
+            sn[i] *= sign;
         }
     }
-
-    const int h_end = min(p.Hq + p.Hk + p.Hv, static_cast<int>(blockIdx.y + 1) * p.heads_per);
-    for (int h0 = blockIdx.y * p.heads_per; h0 < h_end; h0 += kRotUnroll) {
-        Chunk<V> a[kRotUnroll], c[kRotUnroll];
-        __nv_bfloat16* dst[kRotUnroll];
+    auto turn_own = [&](Words<W> (&x)[kChunks]) {  // kHalves, kInterleaved
+        Words<W>& a = x[0];
+        Words<W>& c = x[kChunks - 1];
 #pragma unroll
-        for (int u = 0; u < kRotUnroll; u++) {
-            const int h = h0 + u;
-            dst[u] = nullptr;
-            if (h >= h_end) continue;
-            const __nv_bfloat16* src;
-            if (h < p.Hq) {
-                src = p.q.p + (PAGED ? 0 : b * p.q.batch) + h * p.q.head + n * p.q.token;
-                dst[u] = p.qo.p + (PAGED ? 0 : b * p.qo.batch) + h * p.qo.head + n * p.qo.token;
-            } else if (h < p.Hq + p.Hk) {
-                const int hk = h - p.Hq;
-                src = p.k.p + (PAGED ? 0 : b * p.k.batch) + hk * p.k.head + n * p.k.token;
-                if constexpr (PAGED) {
-                    if (page_off >= 0) dst[u] = p.ko.p + page_off + hk * p.ko.head;
-                } else {
-                    dst[u] = p.ko.p + b * p.ko.batch + hk * p.ko.head + n * p.ko.token;
-                }
+        for (int i = 0; i < 4; i++) {
+            const uint32_t wa = a.w[i], wc = c.w[i];
+            if constexpr (LAYOUT == kInterleaved) {
+                const uint32_t ra = turn_word(wa, __byte_perm(wa, 0, 0x1032), cs[i], cs[i], -sn[i], sn[i]);
+                const uint32_t rc = turn_word(wc, __byte_perm(wc, 0, 0x1032), cs[i + 4], cs[i + 4], -sn[i + 4], sn[i + 4]);
+                a.w[i] = i < n_rot ? ra : wa;
+                c.w[i] = i + 4 < n_rot ? rc : wc;
             } else {
-                const int hv = h - p.Hq - p.Hk;
-                src = p.v.p + hv * p.v.head + n * p.v.token;
-                if (page_off >= 0) dst[u] = p.vo + page_off + hv * p.ko.head;
+                const int j = 2 * i;
+                a.w[i] = turn_word(wa, wc, cs[j], cs[j + 1], -sn[j], -sn[j + 1]);
+                c.w[i] = turn_word(wc, wa, cs[j], cs[j + 1], sn[j], sn[j + 1]);
             }
-            if (dst[u] == nullptr) continue;
-            a[u].load(src + off_a);
-            c[u].load(src + off_b);
         }
+    };
+
+    constexpr int U = rot_unroll(LAYOUT);
+    const int h_begin = static_cast<int>(blockIdx.y) * p.heads_per, h_end = h_begin + p.heads_per;
+    int first = 0;  // heads before this kind's
+#pragma unroll 1
+    for (int kind = 0; kind < (PAGED ? 3 : 2); kind++) {  // queries, keys, values (copied)
+        const RotView& in = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+        const RotView& out = kind == 0 ? p.qo : p.ko;
+        const int heads = kind == 0 ? p.Hq : kind == 1 ? p.Hk : p.Hv;
+        const int h0 = max(h_begin - first, 0), h1 = min(h_end - first, heads);
+        first += heads;
+        const bool paged = PAGED && kind > 0;
+        const bool mine = have && (!paged || page_off >= 0);
+        const __nv_bfloat16* src = in.p + (PAGED ? 0 : b * in.batch) + n * in.token + h0 * in.head + off_a;
+        __nv_bfloat16* dst = (kind == 2 ? p.vo : out.p) + (paged ? page_off : (PAGED ? 0 : b * out.batch) + n * out.token) +
+                             h0 * out.head + off_a;
+        const int d_b = off_b - off_a;
+        const int64_t s_in = in.head, s_out = out.head;
+        auto turn = [&](Words<W> (&x)[kChunks]) {
+            if constexpr (LAYOUT == kShuffled)
+                turn_shuffled<kItems>(x[0], P, lane, cs, sn);
+            else if (n_rot > 0)
+                turn_own(x);
+        };
+        // whole batches of heads, then the rest one by one; lanes without work read nothing and shuffle along
+        int h = h0;
+        for (; h + U <= h1; h += U) {
+            Words<W> x[U][kChunks];
+            if (mine) {
 #pragma unroll
-        for (int u = 0; u < kRotUnroll; u++) {
-            if (dst[u] == nullptr) continue;
-            if (n_rot > 0 && (!PAGED || h0 + u < p.Hq + p.Hk)) rotate_chunks<V, INTER>(a[u], c[u], cs, sn, n_rot);
-            a[u].store(dst[u] + off_a);
-            c[u].store(dst[u] + off_b);
+                for (int u = 0; u < U; u++) {
+                    x[u][0].load(src);
+                    if constexpr (kChunks == 2) x[u][1].load(src + d_b);
+                    src += s_in;
+                }
+            }
+            if (kind < 2) {
+#pragma unroll
+                for (int u = 0; u < U; u++) turn(x[u]);
+            }
+            if (mine) {
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    x[u][0].store(dst);
+                    if constexpr (kChunks == 2) x[u][1].store(dst + d_b);
+                    dst += s_out;
+                }
+            }
+        }
+        for (; h < h1; h++) {
+            Words<W> x[kChunks];
+            if (mine) {
+                x[0].load(src);
+                if constexpr (kChunks == 2) x[1].load(src + d_b);
+            }
+            if (kind < 2) turn(x);
+            if (mine) {
+                x[0].store(dst);
+                if constexpr (kChunks == 2) x[1].store(dst + d_b);
+            }
+            src += s_in;
+            dst += s_out;
         }
     }
 }
