@@ -2,6 +2,7 @@
 // argument checks, kernel choice and launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <initializer_list>
 #include <cmath>
@@ -79,14 +80,15 @@ int rot_launch(const RotSpec& spec, const RotParams& p, bool inter, cudaStream_t
     if (blocks > INT_MAX) return SA_ERR_UNSUPPORTED;
     const int heads = p.Hq + p.Hk + p.Hv;
     RotParams pp = p;
-    // Heads of one thread.  Few tokens: as many parts as the SMs hold blocks, so that all have work.  Many:
-    // parts that make three rounds of blocks, whose ends then even out, but no fewer than 16 heads, over
-    // which the sines are shared.  16 + 16 heads of 128 at 8192 tokens (512 blocks of the 888 held at once):
-    // one part 24.6 us, parts of 16 26.8, of 4 31.6; 64 + 8 heads of 64 at 2 x 16384 (1024 blocks): one part
-    // 109 us, parts of 24 99, of 4 111.
+    // Heads of one thread.  Few tokens: as many parts as the SMs hold blocks, so that all have work, and
+    // three at least.  Many: parts that make three rounds of blocks, whose ends then even out, but no fewer
+    // than 16 heads, over which the sines are shared.  16 + 16 heads of 128 at 8192 tokens (512 blocks of the
+    // 888 held at once): 1 or 3 parts 27.6 us a call, 8 parts 29.9; an append of 64 + 8 + 8 heads of 64 at
+    // 12900 tokens (408 blocks): 2 parts 55.7, 3 51.2, 8 50.1; 64 + 8 heads of 64 at 2 x 16384 (1024 blocks):
+    // 1 part 109 us, 3 parts 99, 18 parts 111.
     const int64_t held = int64_t(rot_blocks(layout)) * device_sm_count();
     const bool few = 3 * blocks <= 2 * held;
-    const int64_t parts = few ? held / blocks : (3 * held + blocks - 1) / blocks;
+    const int64_t parts = few ? (held / blocks > 3 ? held / blocks : 3) : (3 * held + blocks - 1) / blocks;
     int64_t per = (heads + parts - 1) / parts;
     if (!few && per < 16) per = 16;
     per = (per + 3) / 4 * 4;
@@ -310,29 +312,67 @@ bool make_map_pages(CUtensorMap* map, const void* base, const sa_kv_cache& c, ui
 }
 
 // A launch that may be set up while the stream's previous kernel, one of this
-// call's, still runs (it waits for it where it has to).
+// call's, still runs (it waits for it where it has to); in clusters of `cluster`.
 template <typename... Args>
 int launch_after(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool overlap,
-                 const Args&... args)
+                 int cluster, const Args&... args)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute at[2];
+    int n = 0;
+    if (overlap) {
+        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        at[n].id = cudaLaunchAttributeClusterDimension;
+        at[n].val.clusterDim.x = cluster;
+        at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+        n++;
+    }
     cfg.attrs = at;
-    cfg.numAttrs = overlap ? 1 : 0;
+    cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
-template <int D, int MT>
-int launch_decode(const sa_kv_cache& cache, const PassParams& p, bool overlap, cudaStream_t st)
+// How decode_kernel runs a pass: in whole items by clusters of `cluster` CTAs
+// (nothing is left to join), or, cluster 0, over the evenly cut line of units.
+struct DecodePlan {
+    int mt;       // rows of an item: 16 or 32
+    int cluster;
+    int64_t ctas;
+};
+
+// keys: most keys of an item, seqs: sequences, rows: most rows of one, as far as the host knows.
+// Whole items where each CTA then has at most six units: the cut is even for any lengths, but its join
+// costs a launch and some 3 us.
+template <int D>
+DecodePlan plan_decode(int64_t keys, int64_t seqs, int64_t rows, int32_t Hkv)
+{
+    DecodePlan d;
+    d.mt = rows <= 16 ? 1 : 2;
+    const int64_t held = kDecodeCtas * int64_t(device_sm_count());
+    const int64_t items = seqs * Hkv * ((rows + 16 * d.mt - 1) / (16 * d.mt));
+    const int64_t units = keys / DecodeCfg<D, 1>::UK + 3;  // the sinks' and the band's last and first may be partly used
+    int64_t c = 1;
+    while (c < 8 && items * c * 2 <= held && c < units) c *= 2;
+    const bool whole = (units + c - 1) / c <= 6 && items * c <= 4 * held;
+    d.cluster = whole ? static_cast<int>(c) : 0;
+    const int64_t clusters = items < held / c ? items : held / c;
+    d.ctas = whole ? clusters * c : held;
+    return d;
+}
+
+template <int D, int MT, bool ITEMS>
+int launch_decode_as(const sa_kv_cache& cache, const PassParams& p, const DecodePlan& plan, bool overlap,
+                     cudaStream_t st)
 {
     using C = DecodeCfg<D, MT>;
-    auto kern = decode_kernel<D, MT>;
+    auto kern = decode_kernel<D, MT, ITEMS>;
     static bool attr_set[kMaxDevices] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SA_ERR_CUDA;
@@ -345,21 +385,32 @@ int launch_decode(const sa_kv_cache& cache, const PassParams& p, bool overlap, c
     const uint32_t rows = cache.page_size < C::TK ? cache.page_size : C::TK;
     if (!make_map_pages(&mk, cache.k, cache, rows, D / 64) || !make_map_pages(&mv, cache.v, cache, rows, D / 64))
         return SA_ERR_CUDA;
-    return launch_after(kern, dim3(kDecodeCtas * device_sm_count()), C::kThreads, C::kSmemBytes, st, overlap, mk, mv,
-                        p);
+    return launch_after(kern, dim3(static_cast<unsigned>(plan.ctas)), C::kThreads, C::kSmemBytes, st, overlap,
+                        plan.cluster, mk, mv, p);
+}
+
+template <int D>
+int launch_decode(const sa_kv_cache& cache, const PassParams& p, const DecodePlan& plan, bool overlap, cudaStream_t st)
+{
+    if (plan.mt == 1)
+        return plan.cluster ? launch_decode_as<D, 1, true>(cache, p, plan, overlap, st)
+                            : launch_decode_as<D, 1, false>(cache, p, plan, overlap, st);
+    return plan.cluster ? launch_decode_as<D, 2, true>(cache, p, plan, overlap, st)
+                        : launch_decode_as<D, 2, false>(cache, p, plan, overlap, st);
 }
 
 template <int D>
 int launch_join(const JoinParams& j, bool prefix, cudaStream_t st)
 {
-    const int64_t rows = int64_t(j.T) * j.Hq;
-    const int64_t sms = device_sm_count();
-    const bool few = rows <= 8 * sms;
-    const int64_t blocks = few ? rows : (rows + 7) / 8;
-    const dim3 grid(static_cast<unsigned>(blocks < 8 * sms ? blocks : 8 * sms));
-    auto kern = few ? (prefix ? join_kernel<D, 8, true> : join_kernel<D, 8, false>)
-                    : (prefix ? join_kernel<D, 1, true> : join_kernel<D, 1, false>);
-    return launch_after(kern, grid, 256, 0, st, true, j);
+    const int64_t rows = int64_t(j.T) * j.Hq, sms = device_sm_count();
+    // few rows: eight warps each; many: one warp each; very many, most of them finished: a warp looks at eight
+    const int shape = rows <= 8 * sms ? 0 : rows <= 256 * sms || prefix ? 1 : 2;
+    const int64_t blocks = shape == 0 ? rows : shape == 1 ? (rows + 7) / 8 : (rows + 63) / 64;
+    const dim3 grid(static_cast<unsigned>(std::min(blocks, 8 * sms)));
+    auto kern = shape == 0   ? (prefix ? join_kernel<D, 8, 1, true> : join_kernel<D, 8, 1, false>)
+                : shape == 1 ? (prefix ? join_kernel<D, 1, 1, true> : join_kernel<D, 1, 1, false>)
+                             : join_kernel<D, 1, 8, false>;
+    return launch_after(kern, grid, 256, 0, st, true, 1, j);
 }
 
 template <int D>
@@ -383,7 +434,7 @@ int launch_chunk(const sa_kv_cache& cache, const PassParams& p, bool overlap, cu
     const uint32_t rows = cache.page_size < C::UK ? cache.page_size : C::UK;
     if (!make_map_pages(&mk, cache.k, cache, rows, 1) || !make_map_pages(&mv, cache.v, cache, rows, 1))
         return SA_ERR_CUDA;
-    return launch_after(kern, dim3(device_sm_count()), C::kThreads, C::kSmemBytes, st, overlap, mk, mv, p);
+    return launch_after(kern, dim3(device_sm_count()), C::kThreads, C::kSmemBytes, st, overlap, 1, mk, mv, p);
 }
 
 // Part arrays and row entries of one pass, from part row `row0` on.
@@ -408,9 +459,20 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
     const bool prefix = p.prefix_len > 0;
     p.rows_above = 0;
     p.rows_upto = INT_MAX;
-    auto decode = [&](const PassParams& pp, int64_t rows, bool overlap) {
-        return rows <= 16 ? launch_decode<D, 1>(cache, pp, overlap, st) : launch_decode<D, 2>(cache, pp, overlap, st);
+    // most keys of an item, out of `room`: what the window, the sinks and an item's tokens span
+    auto most_keys = [&](int64_t room, int64_t tokens) {
+        if (p.n_global > 0 || p.window < 0) return p.n_global > 0 ? room : std::min<int64_t>(room, p.cols);
+        return std::min<int64_t>(room, int64_t(p.window) + tokens + p.cols);
     };
+    const int64_t room = int64_t(p.max_pages) << p.page_shift;
+    const int64_t most_q = max_q > 0 ? max_q : (int64_t(p.T) + p.B - 1) / p.B;
+    const int64_t rows = most_q * p.group, all_rows = int64_t(p.T) * p.group;
+    const DecodePlan plan = plan_decode<D>(most_keys(room, most_q), p.B, rows, p.Hkv);
+    const DecodePlan over = plan_decode<D>(p.prefix_len, 1, all_rows, p.Hkv);
+    // Nothing is left for join_kernel where each item is finished by its CTAs; over a prefix the sequences'
+    // pass then adds what the prefix's left.
+    const bool finished = rows <= kDecodeRows && plan.cluster > 0 &&
+                          (!prefix || (all_rows <= kDecodeRows && over.cluster > 0));
     if (prefix) {
         // the rows of all sequences against the prefix
         PassParams pp = p;
@@ -418,26 +480,36 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
         pp.table = prefix_table;
         pp.table_stride = 0;
         use_parts(pp, w, ws, 1, w.rows_decode + w.rows_chunk, D, true);
-        const int64_t rows = int64_t(p.T) * p.group;
-        if (int rc = rows <= kDecodeRows ? decode(pp, rows, false) : launch_chunk<D>(cache, pp, false, st)) return rc;
+        if (finished) pp.info = nullptr;
+        if (int rc = all_rows <= kDecodeRows ? launch_decode<D>(cache, pp, over, false, st)
+                                             : launch_chunk<D>(cache, pp, false, st))
+            return rc;
     }
     // each sequence against its own tokens: by decode_kernel alone where no sequence is known to have
     // more than its rows (it can take any), by chunk_kernel alone where there is one sequence of many rows,
     // else by both, each taking the sequences that suit it
-    const int64_t rows = int64_t(max_q > 0 ? max_q : (int64_t(p.T) + p.B - 1) / p.B) * p.group;
-    if (rows <= kDecodeRows || p.B > 1) {
+    if (finished) {
+        if (prefix) {
+            p.pre_acc = reinterpret_cast<const float*>(ws + w.acc[1]);
+            p.pre_ml = reinterpret_cast<const float2*>(ws + w.acc_ml[1]);
+        }
+        return launch_decode<D>(cache, p, plan, prefix, st);
+    }
+    use_parts(p, w, ws, 0, 0, D, prefix);
+    if (rows <= kDecodeRows) {
+        if (int rc = launch_decode<D>(cache, p, plan, prefix, st)) return rc;
+        return launch_join<D>(j, prefix, st);
+    }
+    if (p.B > 1) {
         PassParams pp = p;
-        int64_t most = rows;
-        if (rows > kDecodeRows) most = pp.rows_upto = p.group <= 16 ? 16 : kDecodeRows;
-        use_parts(pp, w, ws, 0, 0, D, prefix);
-        if (int rc = decode(pp, most, prefix)) return rc;
+        pp.rows_upto = p.group <= 16 ? 16 : kDecodeRows;
+        const DecodePlan line{pp.rows_upto <= 16 ? 1 : 2, 0, kDecodeCtas * int64_t(device_sm_count())};
+        if (int rc = launch_decode<D>(cache, pp, line, prefix, st)) return rc;
         p.rows_above = pp.rows_upto;
     }
-    if (rows > kDecodeRows) {
-        const bool overlap = prefix || p.B > 1;
-        use_parts(p, w, ws, 0, w.rows_decode, D, prefix);
-        if (int rc = launch_chunk<D>(cache, p, overlap, st)) return rc;
-    }
+    const bool overlap = prefix || p.B > 1;
+    use_parts(p, w, ws, 0, w.rows_decode, D, prefix);
+    if (int rc = launch_chunk<D>(cache, p, overlap, st)) return rc;
     return launch_join<D>(j, prefix, st);
 }
 
@@ -489,6 +561,12 @@ int fwd_paged(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* 
     p.Hq = Hq;
     p.Hkv = cache->Hkv;
     p.group = Hq / cache->Hkv;
+    // the kernels count units of 64 keys or more of 16 rows or more in 31 bits
+    const int64_t most = std::max<int64_t>(int64_t(batch->max_pages) * cache->page_size, prefix_len) / 64 + 3;
+    if ((int64_t(T) * p.group / 16 + batch->B) * most > INT_MAX / int64_t(p.Hkv)) return SA_ERR_UNSUPPORTED;
+    while ((int64_t(1) << p.group_shift) < p.group) p.group_shift++;
+    p.group_shift += 31;
+    p.group_mul = static_cast<uint32_t>((uint64_t(1) << p.group_shift) / p.group + 1);
     p.n_pages = cache->n_pages;
     p.page_shift = page_shift_of(cache->page_size);
     p.max_pages = batch->max_pages;

@@ -40,8 +40,7 @@ struct ChunkCfg {
     static constexpr int kPanel = 128 * 128;                 // 64 columns x 128 rows
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kOffRing = 2 * kQBytes;
-    static constexpr int kOffScan = kOffRing + kStages * kTileBytes;
-    static constexpr int kOffBar = kOffScan + 16 * 8;
+    static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
     static constexpr int kNumBars = 2 * kStages + 2 * 6 + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kSmemUsed = kOffMisc + 16;
@@ -67,7 +66,6 @@ __global__ void __launch_bounds__(384, 1)
     extern __shared__ __align__(1024) uint8_t smem[];  // swizzled tiles sit on 1024 bytes
     uint8_t* sQ = smem;
     uint8_t* ring = smem + C::kOffRing;
-    int64_t* scan = reinterpret_cast<int64_t*>(smem + C::kOffScan);
     uint64_t* ring_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [S]
     uint64_t* ring_empty = ring_full + S;                                  // [S]
     uint64_t* q_full = ring_empty + S;   // [2]
@@ -108,14 +106,14 @@ __global__ void __launch_bounds__(384, 1)
         tma_prefetch_desc(&tmV);
     }
     launch_dependents();
-    const Piece piece = find_piece<R, UK, C::kThreads>(p, 1, scan);
+    const Piece piece = find_piece<R, UK, false>(p, peek_seq(p), blockIdx.x, gridDim.x);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const long long lim = p.timeout;
     const int n_seq = p.over_prefix ? 1 : p.B;
-    const int total = static_cast<int>(piece.u1 - piece.u0);
+    const int total = piece.u1 - piece.u0;
     auto fail = [&]() {
         *abort_flag = 1;
         atomicOr(p.status, ST_PAGED_WAIT);
@@ -152,7 +150,7 @@ __global__ void __launch_bounds__(384, 1)
                     const int box = lane / P, panel = lane % P;
                     const bool mine = box < nb;
                     const int k = k0 + box * page_rows;
-                    const int pg = mine ? page_of(p, c, k) : 0;
+                    const int pg = mine ? page_of(p, c.b, k) : 0;
                     const int row = k & ((1 << p.page_shift) - 1);
 #pragma unroll
                     for (int v = 0; v < 2; v++) {  // K, then V
@@ -300,7 +298,7 @@ __global__ void __launch_bounds__(384, 1)
                     for (int r = lane / L; r < 128; r += RW) {
                         // rows behind the item's last repeat it: what they compute is not written
                         const int rr = c.rb * R + x * 128 + min(r, rows - 1);
-                        const int i = rr / p.group, g = rr % p.group;
+                        const int i = div_group(p, rr), g = rr - i * p.group;
                         cp_async_16(dst0 + (ch / 8) * C::kPanel + r * 128 + (((ch % 8) ^ (r & 7)) * 16),
                                     p.q + (c.s.first + i) * p.q_token + (c.h * p.group + g) * p.q_head + ch * 8);
                     }
@@ -337,12 +335,12 @@ __global__ void __launch_bounds__(384, 1)
             }
             const int r0 = c.rb * R + x * 128;
             const int rr = r0 + min(row, rows - 1);
-            const int i_tok = rr / p.group;
+            const int i_tok = div_group(p, rr);
             const int base = p.prefix_len + c.s.p0;
             // the slot's lowest and highest position, this row's, and the item's (whose keys are loaded)
-            const int p_lo = p.over_prefix ? piece.pb.lo : base + r0 / p.group;
-            const int p_hi = p.over_prefix ? piece.pb.hi : base + (r0 + min(rows, 128) - 1) / p.group;
-            const int item_hi = p.over_prefix ? piece.pb.hi : base + (c.rb * R + rows_of_item() - 1) / p.group;
+            const int p_lo = p.over_prefix ? piece.pb.lo : base + div_group(p, r0);
+            const int p_hi = p.over_prefix ? piece.pb.hi : base + div_group(p, r0 + min(rows, 128) - 1);
+            const int item_hi = p.over_prefix ? piece.pb.hi : base + div_group(p, c.rb * R + rows_of_item() - 1);
             const bool look_up = p.over_prefix && !(p_lo >= p.prefix_len - 1 && p.window >= 0 && p_hi <= p.window);
             const int pr = look_up ? token_position(p, c.s.first + i_tok) : p.over_prefix ? p_lo : base + i_tok;
             const bool row_all = pr < p.n_global;
@@ -497,19 +495,19 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive(&o_empty[x]);
             segs++;
             if (row < rows) {
-                const int64_t u_item = piece.u0 + (total - left) - c.i;
-                const int c_first = cta_of(piece, u_item), c_last = cta_of(piece, u_item + c.u.nt - 1);
-                const bool whole = c_first == c_last;
-                const bool begins = c_first == static_cast<int>(blockIdx.x);
+                const int u_item = piece.u0 + (total - left) - c.i;
+                const bool begins = u_item >= piece.u0, whole = begins && u_item + c.u.nt <= piece.u1;
                 const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0)) * R + x * 128 + row;
                 const int64_t t = c.s.first + i_tok;
-                const int hq = c.h * p.group + rr % p.group;
+                const int hq = c.h * p.group + rr - i_tok * p.group;
                 const int64_t at = t * p.Hq + hq;
                 if (begins) {
                     RowInfo ri{0, 0, 0, 0};
-                    if (!whole)
-                        ri = RowInfo{p.part_row0 + static_cast<int32_t>(slot),
-                                     p.part_row0 + (2 * c_first + 2) * R + x * 128 + row, c_last - c_first + 1, 2 * R};
+                    if (!whole) {
+                        const int n_parts = cta_of(piece, u_item + c.u.nt - 1) - static_cast<int>(blockIdx.x) + 1;
+                        ri = RowInfo{p.part_row0 + static_cast<int32_t>(slot), p.part_row0 + static_cast<int32_t>(slot) + R,
+                                     n_parts, 2 * R};
+                    }
                     p.info[at] = ri;
                 }
                 if (whole && p.acc == nullptr) {

@@ -3,18 +3,32 @@
 //
 // Each key and value is read once for at most 32 rows: 4 bytes of cache carry 4 R
 // operations, far below what the tensor cores need to be the limit, so the kernel
-// is bound by memory and everything serves to keep loads in flight.  Four warps
-// of a CTA work without a barrier between them: each has its own ring of stages
-// (8 KB: TK keys and values), loads its own tiles with one TMA per page, S = Q K^T
-// and O += P V on mma.sync with R = 16 MT rows, and its own running maximum and
-// sum; the warps meet only where an item ends.  A warp's loads run ahead over the
-// borders of items.  Two CTAs of an SM hold 8 warps x 3 stages x 8 KB = 192 KB in
-// flight (two stages for MT = 2), four times what HBM's latency asks for.
+// is bound by memory, and small calls by latency.  Four warps of a CTA work
+// without a barrier between them: each has its own ring of stages (8 KB: TK keys
+// and values), loads its own tiles with one TMA per page, S = Q K^T and O += P V
+// on mma.sync with R = 16 MT rows, and its own running maximum and sum; the warps
+// meet only where an item ends.  A warp's loads run ahead over the borders of
+// items.  Two CTAs of an SM hold 8 warps x 3 stages x 8 KB = 192 KB in flight (two
+// stages for MT = 2), four times what HBM's latency asks for.  64 sequences of 550
+// to 16384 tokens, 32/8 heads of 128: 204 us, 6.06 TB/s.
 //
 // mma.sync, not tcgen05: 16 rows fill its tile, and its operands come straight
 // from registers; a 128-row tcgen05 tile would be 7/8 padding and would pay the
 // trip through tensor memory for every tile of 16 keys.
+//
+// ITEMS = false: the line of units is cut evenly (see paged_sm100.cuh), cut items
+// are joined by join_kernel.  ITEMS = true, for items of few units: a cluster of
+// CTAs takes whole items, its CTAs every n-th unit of one, and the parts are added
+// over distributed shared memory, so that nothing has to follow.
+//
+// Code that runs once in a launch costs about 9 cycles an instruction (it comes
+// from L2: measured on the first and second pass over the same tile, 8660 and 1580
+// cycles), more than the data of a small call.  So the once-run parts are short:
+// rolled loops, no division, one copy of the walk over the items, which the
+// loading side leaves to the other in a record per stage.
 #pragma once
+
+#include <type_traits>
 
 #include "paged_sm100.cuh"
 
@@ -42,6 +56,47 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Clusters: this CTA's place, the two halves of a barrier over all their threads
+// (release, acquire), and stores to a CTA's shared memory.
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_st4(uint32_t addr, uint32_t rank, float4 v)
+{
+    asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+                 "st.shared::cluster.v4.f32 [a], {%2, %3, %4, %5};\n\t}" ::"r"(addr),
+                 "r"(rank), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_st2(uint32_t addr, uint32_t rank, float2 v)
+{
+    asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+                 "st.shared::cluster.v2.f32 [a], {%2, %3};\n\t}" ::"r"(addr),
+                 "r"(rank), "f"(v.x), "f"(v.y)
+                 : "memory");
+}
+
+// What the loading side of a warp knows about a stage's tile.
+struct alignas(16) TileRec {
+    int32_t k0;            // first key of the warp's tile
+    int32_t unit;          // unit of the item (below 2^24), the item's last tile of this CTA (bit 24), its rows (above)
+    int32_t nt;            // the item's units
+    int32_t hi;            // its keys end before hi
+    int32_t first, rb, h;  // the sequence's first token, row block, head
+    int32_t base;          // position of the sequence's first new token
+};
+
 template <int D, int MT>
 struct DecodeCfg {
     static constexpr int kWarps = 4;
@@ -53,103 +108,145 @@ struct DecodeCfg {
     static constexpr int kTileBytes = TK * D * 2;
     static constexpr int kPanel = TK * 128;     // 64 columns x TK rows
     static constexpr int kOffMerge = kWarps * kStages * 2 * kTileBytes;
-    static constexpr int kOffMl = kOffMerge + 2 * R * D * 4;  // two warps' O
-    static constexpr int kOffScan = kOffMl + 2 * kWarps * R * 4;
-    static constexpr int kOffBar = kOffScan + 16 * 8;
-    static constexpr int kSmem = kOffBar + kWarps * kStages * 8;
-    static constexpr int kSmemBytes = kSmem;
+    static constexpr int kOffMl = kOffMerge + 2 * R * D * 4;     // two warps' O
+    static constexpr int kOffRec = kOffMl + 2 * kWarps * R * 4;  // the warps' maxima and sums
+    static constexpr int kOffBar = kOffRec + kWarps * kStages * static_cast<int>(sizeof(TileRec));
+    static constexpr int kSmemBytes = kOffBar + kWarps * kStages * 8;
     static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
-template <int D, int MT>
+template <int D, int MT, bool ITEMS>
 __global__ void __launch_bounds__(128, 2)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ PassParams p)
 {
     using C = DecodeCfg<D, MT>;
     constexpr int R = C::R, TK = C::TK, UK = C::UK, ST = C::kStages, NW = C::kWarps;
+    constexpr int NF = D / 32;  // mma column tiles of a warp's quarter of the columns
     extern __shared__ __align__(1024) uint8_t smem[];  // swizzled tiles sit on 1024 bytes
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     uint8_t* ring = smem + warp * ST * 2 * C::kTileBytes;
-    float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
-    float* sm_m = reinterpret_cast<float*>(smem + C::kOffMl);  // [NW][R]
+    float4* merge = reinterpret_cast<float4*>(smem + C::kOffMerge);  // [2][MT][D / 8][32 lanes]
+    float* sm_m = reinterpret_cast<float*>(smem + C::kOffMl);        // [NW][R]
     float* sm_l = sm_m + NW * R;
-    int64_t* scan = reinterpret_cast<int64_t*>(smem + C::kOffScan);
+    TileRec* recs = reinterpret_cast<TileRec*>(smem + C::kOffRec) + warp * ST;
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * ST;
 
+    launch_dependents();
+    const SeqView ahead = peek_seq(p);  // on its way while the barriers are set up
     if (lane == 0) {
         for (int s = 0; s < ST; s++) mbar_init(&bar[s], 1);
         fence_barrier_init();
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
     }
     __syncwarp();
-    launch_dependents();
-    const Piece piece = find_piece<R, UK, C::kThreads>(p, 1, scan);
-    const int n = static_cast<int>(piece.u1 - piece.u0);
-    if (n <= 0) {
+    const int rank = ITEMS ? static_cast<int>(cluster_rank()) : 0;
+    const int CL = ITEMS ? static_cast<int>(cluster_size()) : 1;
+    const Piece piece = ITEMS ? find_piece<R, UK, true>(p, ahead, blockIdx.x / CL, gridDim.x / CL)
+                              : find_piece<R, UK, false>(p, ahead, blockIdx.x, gridDim.x);
+    const int n_seq = p.over_prefix ? 1 : p.B;
+
+    // ---- loads: this warp's tile of every unit of the piece, ST tiles ahead
+    const int page_rows = min(1 << p.page_shift, TK);  // rows of one box
+    Cursor pc = piece.c;
+    if (ITEMS) pc.i = rank;
+    int left = piece.u1 - piece.u0;  // units (items) to come
+    int issued = 0, live = 0;  // tiles, and those loaded (a warp whose wait ran out goes on without loads)
+    bool dead = false;
+    // The next tile is looked up one step before its loads go out, so that its page numbers are there by then.
+    struct Next {
+        TileRec rec;
+        int nb, k, page;  // boxes to load; this lane's
+        bool any;
+    } nx;
+    auto look_up_next = [&]() {
+        nx.any = left > 0;
+        if (!nx.any) return;
+        const int k0 = pc.u.key(pc.i, UK) + warp * TK;
+        // boxes that begin below the item's last key; a tile with none completes its phase at once
+        nx.nb = min((pc.u.hi - k0 + page_rows - 1) / page_rows, TK / page_rows);
+        if (nx.nb < 0 || pc.i >= pc.u.nt) nx.nb = 0;  // ITEMS: a CTA may have no unit of an item
+        nx.k = k0 + lane * page_rows;
+        nx.page = lane < nx.nb ? page_of(p, pc.b, nx.k) : 0;
+        const bool last = pc.i + CL >= pc.u.nt || (!ITEMS && left == 1);
+        const int rows = min(pc.s.m * p.group - pc.rb * R, R);
+        nx.rec = TileRec{nx.nb > 0 ? k0 : INT32_MAX, pc.i | (last ? 1 << 24 : 0) | rows << 25, pc.u.nt, pc.u.hi,
+                         pc.s.first, pc.rb, pc.h, p.prefix_len + pc.s.p0};
+        if (!ITEMS || last) left--;
+        pc.i += CL;
+        if (pc.i >= pc.u.nt && left > 0) {
+            next_item<R, UK>(p, piece.pb, pc, n_seq);
+            if (ITEMS) pc.i = rank;
+        }
+    };
+    auto issue = [&]() {
+        const Next now = nx;
+        look_up_next();
+        const int st = issued % ST;
+        const bool skip = (p.debug_flags & 1) && blockIdx.x == 0 && warp == 0 && issued == 0;
+        if (lane == 0) {
+            recs[st] = now.rec;
+            if (!dead) mbar_arrive_expect_tx(&bar[st], skip ? 16 : now.nb * page_rows * D * 4);
+        }
+        __syncwarp();
+        if (lane < now.nb && !skip && !dead) {
+            uint8_t* k_dst = ring + st * 2 * C::kTileBytes + lane * page_rows * 128;
+            const int row = now.k & ((1 << p.page_shift) - 1);
+            tma_load_5d(k_dst, &tmK, &bar[st], 0, row, 0, now.rec.h, now.page);
+            tma_load_5d(k_dst + C::kTileBytes, &tmV, &bar[st], 0, row, 0, now.rec.h, now.page);
+        }
+        issued++;
+        if (!dead) live = issued;
+    };
+    look_up_next();
+    if (!nx.any) {
         wait_previous_kernel();
         return;
     }
-    const int n_seq = p.over_prefix ? 1 : p.B;
 
-    // ---- loads: this warp's tile of every unit of the piece, ST units ahead
-    const int page_rows = min(1 << p.page_shift, TK);  // rows of one box
-    const int boxes = TK / page_rows;
-    Cursor pc = piece.c;
-    int issued = 0;
-    bool dead = false;
-    auto issue = [&]() {
-        const int st = issued % ST;
-        uint8_t* k_dst = ring + st * 2 * C::kTileBytes;
-        const int k0 = pc.u.key(pc.i, UK) + warp * TK;
-        // boxes that begin below the item's last key; a tile with none completes its phase at once
-        const int nb = min(max((pc.u.hi - k0 + page_rows - 1) / page_rows, 0), boxes);
-        const bool skip = (p.debug_flags & 1) && blockIdx.x == 0 && warp == 0 && issued == 0;
-        if (lane == 0) mbar_arrive_expect_tx(&bar[st], skip ? 16 : nb * page_rows * D * 4);
-        __syncwarp();
-        if (lane < nb && !skip) {
-            const int k = k0 + lane * page_rows;
-            const int pg = page_of(p, pc, k);
-            const int row = k & ((1 << p.page_shift) - 1);
-            tma_load_5d(k_dst + lane * page_rows * 128, &tmK, &bar[st], 0, row, 0, pc.h, pg);
-            tma_load_5d(k_dst + C::kTileBytes + lane * page_rows * 128, &tmV, &bar[st], 0, row, 0, pc.h, pg);
-        }
-        issued++;
-        if (++pc.i >= pc.u.nt) next_item<R, UK>(p, piece.pb, pc, n_seq);
-    };
-    for (int j = 0; j < ST && j < n; j++) issue();
-
-    // ---- the piece's units
-    Cursor c = piece.c;
+    // ---- the piece's tiles
     const int rq = lane / 4, cq = (lane % 4) * 2;  // this lane's row (and row + 8) and column pair in an mma tile
+    const int off = p.over_prefix ? 0 : p.prefix_len;  // position of key 0
     uint32_t qf[MT][D / 16][4];
     float o[MT][D / 8][4];
     float m_ref[MT][2], l_sum[MT][2];
-    int pos[MT][2];           // positions of this lane's rows
-    int p_lo = 0, p_hi = 0;   // the item's lowest and highest
+    int row_lo[MT][2], row_hi[MT][2];  // keys this lane's rows see: row_lo .. row_hi, and those below cols
+    const int cols = p.cols - off;
+    TileRec it;                        // of the item
+    int lo_lo = 0, lo_hi = 0, hi_lo = 0, hi_hi = 0;  // lowest and highest of the rows' bounds
     int rows_left = 0;
-    const int off = p.over_prefix ? 0 : p.prefix_len;
     bool fresh = true;
-    for (int j = 0; j < n; j++) {
+    issue();
+#pragma unroll 1
+    for (int j = 0; j < issued; j++) {
+        const int st = j % ST;
         if (fresh) {
-            // Q fragments of the item's rows, straight from memory
-            const int r0 = c.rb * R;
-            rows_left = min(c.s.m * p.group - r0, R);
-            const int base = p.prefix_len + c.s.p0;
-            p_lo = p.over_prefix ? piece.pb.lo : base + r0 / p.group;
-            p_hi = p.over_prefix ? piece.pb.hi : base + (r0 + rows_left - 1) / p.group;
+            fresh = false;
+            it = recs[st];
+            const int r0 = it.rb * R;
+            rows_left = it.unit >> 25;
+            const int p_lo = p.over_prefix ? piece.pb.lo : it.base + div_group(p, r0);
+            const int p_hi = p.over_prefix ? piece.pb.hi : it.base + div_group(p, r0 + rows_left - 1);
+            auto first_seen = [&](int pos) {
+                return pos < p.n_global ? 0 : p.window >= 0 ? pos - p.window - off : INT32_MAX;
+            };
+            lo_lo = first_seen(p_lo);
+            lo_hi = first_seen(p_hi);
+            hi_lo = min(p_lo - off, it.hi - 1);
+            hi_hi = min(p_hi - off, it.hi - 1);
             // over the prefix the rows' own positions matter unless every row sees every key
             const bool look_up = p.over_prefix && !(p_lo >= p.prefix_len - 1 && p.window >= 0 && p_hi <= p.window);
+            // Q fragments of the item's rows, straight from memory
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
 #pragma unroll
                 for (int x = 0; x < 2; x++) {
                     const int r = mt * 16 + rq + 8 * x;
                     const int rr = r0 + min(r, rows_left - 1);
-                    const int i = rr / p.group, g = rr % p.group;
-                    pos[mt][x] = look_up ? token_position(p, c.s.first + i) : p.over_prefix ? p_lo : base + i;
-                    const __nv_bfloat16* src = p.q + (c.s.first + i) * p.q_token + (c.h * p.group + g) * p.q_head + cq;
+                    const int i = div_group(p, rr), g = rr - i * p.group;
+                    const int pos = look_up ? token_position(p, it.first + i) : p.over_prefix ? p_lo : it.base + i;
+                    row_lo[mt][x] = first_seen(pos);
+                    row_hi[mt][x] = min(pos - off, it.hi - 1);
+                    const __nv_bfloat16* src = p.q + (it.first + i) * p.q_token + (it.h * p.group + g) * p.q_head + cq;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; kk++)
 #pragma unroll
@@ -165,38 +262,35 @@ __global__ void __launch_bounds__(128, 2)
                 for (int i = 0; i < D / 8; i++)
 #pragma unroll
                     for (int e = 0; e < 4; e++) o[mt][i][e] = 0.f;
-            fresh = false;
         }
-        const int st = j % ST;
+        // tiles up to ST ahead: the stage of the last one has just been read
+#pragma unroll 1
+        while (issued < j + ST && nx.any) issue();
+        const int k0 = recs[st].k0, packed = recs[st].unit;
+        const int unit = packed & 0xffffff;
+        const bool last = (packed >> 24) & 1;
         if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar[st], (j / ST) & 1, p.timeout))) {
             dead = true;
             if (lane == 0) atomicOr(p.status, ST_PAGED_WAIT);
         }
-        const int k0 = c.u.key(c.i, UK) + warp * TK;
-        if (!dead && k0 < c.u.hi) {
+        if (!dead && k0 < it.hi) {
             const uint32_t ks = smem_addr(ring + st * 2 * C::kTileBytes);
             const uint32_t vs = ks + C::kTileBytes;
-            // positions of the tile's first and last key; is every key seen by every row?
-            const int a = k0 + off, z = a + TK - 1;
-            const bool full = k0 + TK <= c.u.hi && z <= p_lo &&
-                              ((p.window >= 0 && p_hi - a <= p.window) || z < p.cols || p_hi < p.n_global);
-            if (!full) {
-                // values no row sees may be anything, and 0 x infinity is not 0: clear them
-                const bool mine = lane < TK;
-                const int kp = a + lane;
-                const bool seen = k0 + lane < c.u.hi && kp <= p_hi &&
-                                  (kp < p.cols || p_lo < p.n_global || (p.window >= 0 && p_lo - kp <= p.window));
-                if (mine && !seen) {
-                    uint8_t* v = ring + st * 2 * C::kTileBytes + C::kTileBytes + lane * 128;
+            // is every key of the tile seen by every row?
+            const int z = k0 + TK - 1;
+            const bool full = z <= hi_lo && (k0 >= lo_hi || z < cols);
+            // Values no row sees may be anything, and 0 x infinity is not 0: such keys' halves of the V fragments
+            // are cleared (the masks are all ones in a full tile; clearing shared memory instead took longer).
+            uint32_t keep[TK / 16][2];
 #pragma unroll
-                    for (int pn = 0; pn < D / 64; pn++)
+            for (int kb = 0; kb < TK / 16; kb++)
 #pragma unroll
-                        for (int x = 0; x < 8; x++)
-                            *reinterpret_cast<uint4*>(v + pn * C::kPanel + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                for (int y = 0; y < 2; y++) {
+                    const int kp = k0 + kb * 16 + y * 8 + cq;
+                    const bool a = full || (kp <= hi_hi && (kp >= lo_lo || kp < cols));
+                    const bool b = full || (kp + 1 <= hi_hi && (kp + 1 >= lo_lo || kp + 1 < cols));
+                    keep[kb][y] = (a ? 0xffffu : 0u) | (b ? 0xffff0000u : 0u);
                 }
-                fence_proxy_async_smem();  // before the copy that refills the stage
-                __syncwarp();
-            }
             float s[MT][TK / 8][4];
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
@@ -226,11 +320,9 @@ __global__ void __launch_bounds__(128, 2)
                     for (int nb = 0; nb < TK / 8; nb++)
 #pragma unroll
                         for (int e = 0; e < 4; e++) {
-                            const int kk = nb * 8 + cq + (e & 1);
-                            const int kp = a + kk, pr = pos[mt][e >> 1];
-                            const bool seen = k0 + kk < c.u.hi && kp <= pr &&
-                                              (kp < p.cols || pr < p.n_global || (p.window >= 0 && pr - kp <= p.window));
-                            if (!seen) s[mt][nb][e] = -INFINITY;
+                            const int kp = k0 + nb * 8 + cq + (e & 1);
+                            if (!(kp <= row_hi[mt][e >> 1] && (kp >= row_lo[mt][e >> 1] || kp < cols)))
+                                s[mt][nb][e] = -INFINITY;
                         }
             }
             // running maximum (a row's four lanes agree), weights, sum
@@ -243,23 +335,21 @@ __global__ void __launch_bounds__(128, 2)
                     mx[0] = fmaxf(mx[0], fmaxf(s[mt][nb][0], s[mt][nb][1]));
                     mx[1] = fmaxf(mx[1], fmaxf(s[mt][nb][2], s[mt][nb][3]));
                 }
+                float al[2];
+                bool scale_o = false;
 #pragma unroll
                 for (int x = 0; x < 2; x++) {
                     mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
                     mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2)) * p.scale_log2;
+                    // the reference follows the maximum only when it grows by 2^8 (as it may: O and the sum
+                    // carry the same reference), so O is rarely rescaled
+                    const bool grow = mx[x] > m_ref[mt][x] + 8.f;
+                    al[x] = grow ? ex2_approx(m_ref[mt][x] - mx[x]) : 1.f;
+                    scale_o = scale_o || (grow && m_ref[mt][x] != -INFINITY);  // before that O is 0
+                    if (grow) m_ref[mt][x] = mx[x];
+                    l_sum[mt][x] *= al[x];
                 }
-                // the reference follows the maximum only when it grows by 2^8 (as it may: O and the
-                // sum carry the same reference), so O is rarely rescaled
-                const bool grow = mx[0] > m_ref[mt][0] + 8.f || mx[1] > m_ref[mt][1] + 8.f;
-                if (__any_sync(0xffffffffu, grow)) {
-                    float al[2];
-#pragma unroll
-                    for (int x = 0; x < 2; x++) {
-                        const float mn = fmaxf(m_ref[mt][x], mx[x]);
-                        al[x] = mn == -INFINITY ? 1.f : ex2_approx(m_ref[mt][x] - mn);
-                        m_ref[mt][x] = mn;
-                        l_sum[mt][x] *= al[x];
-                    }
+                if (__any_sync(0xffffffffu, scale_o)) {
 #pragma unroll
                     for (int i = 0; i < D / 8; i++) {
                         o[mt][i][0] *= al[0];
@@ -293,139 +383,211 @@ __global__ void __launch_bounds__(128, 2)
                     uint32_t b[4];
                     ldsm_x4_t(vs + (d * 16 / 64) * C::kPanel + row * 128 + ((ch ^ (row & 7)) * 16), b);
 #pragma unroll
+                    for (int y = 0; y < 4; y++) b[y] &= keep[kb][y & 1];
+#pragma unroll
                     for (int mt = 0; mt < MT; mt++) {
                         mma_16816(o[mt][2 * d], pf[mt][kb], b[0], b[1]);
                         mma_16816(o[mt][2 * d + 1], pf[mt][kb], b[2], b[3]);
                     }
                 }
         }
-        __syncwarp();  // the stage is read: refill it
-        if (issued < n && !dead) issue();
+        __syncwarp();  // the stage is read
+        if (!last) continue;
 
-        const bool item_end = c.i + 1 >= c.u.nt;
-        if (item_end || j + 1 == n) {
-            // ---- join the warps: common maximum, then the O's over two rounds
+        // ---- the item's last tile here: add the four warps.  Each warp's O goes to shared memory, two warps
+        // at a time, and each warp sums a quarter of the columns, weighted by 2^(its maximum - the common one).
 #pragma unroll
-            for (int mt = 0; mt < MT; mt++)
+        for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-                for (int x = 0; x < 2; x++) {
-                    l_sum[mt][x] += __shfl_xor_sync(0xffffffffu, l_sum[mt][x], 1);
-                    l_sum[mt][x] += __shfl_xor_sync(0xffffffffu, l_sum[mt][x], 2);
-                    if (lane % 4 == 0) {
-                        sm_m[warp * R + mt * 16 + rq + 8 * x] = m_ref[mt][x];
-                        sm_l[warp * R + mt * 16 + rq + 8 * x] = l_sum[mt][x];
-                    }
+            for (int x = 0; x < 2; x++) {
+                l_sum[mt][x] += __shfl_xor_sync(0xffffffffu, l_sum[mt][x], 1);
+                l_sum[mt][x] += __shfl_xor_sync(0xffffffffu, l_sum[mt][x], 2);
+                if (lane % 4 == 0) {
+                    sm_m[warp * R + mt * 16 + rq + 8 * x] = m_ref[mt][x];
+                    sm_l[warp * R + mt * 16 + rq + 8 * x] = l_sum[mt][x];
                 }
-            __syncthreads();
-            float M[MT][2], L[MT][2];
+            }
+        float M[MT][2], L[MT][2], acc[MT][NF][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; mt++)
+        for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-                for (int x = 0; x < 2; x++) {
-                    const int r = mt * 16 + rq + 8 * x;
-                    float mm = -INFINITY;
+            for (int i = 0; i < NF; i++)
 #pragma unroll
-                    for (int w = 0; w < NW; w++) mm = fmaxf(mm, sm_m[w * R + r]);
-                    float ll = 0.f;
-#pragma unroll
-                    for (int w = 0; w < NW; w++) {
-                        const float mw = sm_m[w * R + r];
-                        if (mw != -INFINITY) ll += sm_l[w * R + r] * ex2_approx(mw - mm);
-                    }
-                    M[mt][x] = mm;
-                    L[mt][x] = ll;
-                    const float f = m_ref[mt][x] == -INFINITY ? 0.f : ex2_approx(m_ref[mt][x] - mm);
-#pragma unroll
-                    for (int i = 0; i < D / 8; i++) {
-                        o[mt][i][2 * x] *= f;
-                        o[mt][i][2 * x + 1] *= f;
-                    }
-                }
-            auto put = [&](float* dst) {
+                for (int e = 0; e < 4; e++) acc[mt][i][e] = 0.f;
+#pragma unroll 1
+        for (int half = 0; half < 2; half++) {
+            if (warp / 2 == half) {
 #pragma unroll
                 for (int mt = 0; mt < MT; mt++)
 #pragma unroll
                     for (int i = 0; i < D / 8; i++)
-                        *reinterpret_cast<float4*>(dst + ((mt * (D / 8) + i) * 32 + lane) * 4) =
+                        merge[(((warp & 1) * MT + mt) * (D / 8) + i) * 32 + lane] =
                             make_float4(o[mt][i][0], o[mt][i][1], o[mt][i][2], o[mt][i][3]);
-            };
-            auto add = [&](const float* src) {
-#pragma unroll
-                for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-                    for (int i = 0; i < D / 8; i++) {
-                        const float4 v =
-                            *reinterpret_cast<const float4*>(src + ((mt * (D / 8) + i) * 32 + lane) * 4);
-                        o[mt][i][0] += v.x;
-                        o[mt][i][1] += v.y;
-                        o[mt][i][2] += v.z;
-                        o[mt][i][3] += v.w;
-                    }
-            };
-            if (warp >= 2) put(merge + (warp - 2) * R * D);
+            }
             __syncthreads();
-            if (warp < 2) add(merge + warp * R * D);
-            if (warp == 1) put(merge + R * D);
-            __syncthreads();
-            if (warp == 0) {
-                add(merge + R * D);
-                // the item's units are [u_item, u_item + nt); is it all in this piece?
-                const int64_t u_now = piece.u0 + j;
-                const int64_t u_item = u_now - c.i;
-                const int c_first = cta_of(piece, u_item), c_last = cta_of(piece, u_item + c.u.nt - 1);
-                const bool whole = c_first == c_last;
-                const bool begins = c_first == static_cast<int>(blockIdx.x);
-                const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0)) * R;
+            if (half == 0) {
 #pragma unroll
                 for (int mt = 0; mt < MT; mt++)
 #pragma unroll
                     for (int x = 0; x < 2; x++) {
                         const int r = mt * 16 + rq + 8 * x;
-                        if (r >= rows_left) continue;
-                        const int rr = c.rb * R + r;
-                        const int64_t t = c.s.first + rr / p.group;
-                        const int hq = c.h * p.group + rr % p.group;
-                        const int64_t at = t * p.Hq + hq;
-                        if (begins && lane % 4 == 0) {
-                            RowInfo ri{0, 0, 0, 0};
-                            if (!whole)
-                                ri = RowInfo{p.part_row0 + static_cast<int32_t>(slot) + r,
-                                             p.part_row0 + (2 * c_first + 2) * R + r, c_last - c_first + 1, 2 * R};
-                            p.info[at] = ri;
-                        }
-                        if (whole && p.acc == nullptr) {
-                            const float inv = L[mt][x] > 0.f ? 1.f / L[mt][x] : 0.f;
-                            __nv_bfloat16* dst = p.o + t * p.o_token + hq * p.o_head + cq;
-#pragma unroll
-                            for (int i = 0; i < D / 8; i++)
-                                *reinterpret_cast<uint32_t*>(dst + i * 8) =
-                                    pack_bf16x2(o[mt][i][2 * x] * inv, o[mt][i][2 * x + 1] * inv);
-                            if (lane % 4 == 0)
-                                p.lse[at] = L[mt][x] > 0.f ? (M[mt][x] + log2f(L[mt][x])) * 0.69314718055994530942f
-                                                           : -INFINITY;
-                        } else {
-                            float* dst = (whole ? p.acc + at * D : p.part_o + (slot + r) * D) + cq;
-#pragma unroll
-                            for (int i = 0; i < D / 8; i++)
-                                *reinterpret_cast<float2*>(dst + i * 8) =
-                                    make_float2(o[mt][i][2 * x], o[mt][i][2 * x + 1]);
-                            if (lane % 4 == 0)
-                                (whole ? p.acc_ml[at] : p.part_ml[slot + r]) = make_float2(M[mt][x], L[mt][x]);
-                        }
+                        M[mt][x] = fmaxf(fmaxf(sm_m[r], sm_m[R + r]), fmaxf(sm_m[2 * R + r], sm_m[3 * R + r]));
+                        L[mt][x] = 0.f;
                     }
             }
-            // the merge buffers are written again only after the next item's first barrier
-            fresh = true;
+#pragma unroll 1
+            for (int w = 2 * half; w < 2 * half + 2; w++) {
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++) {
+                    float f[2];
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        const int r = w * R + mt * 16 + rq + 8 * x;
+                        f[x] = sm_m[r] == -INFINITY ? 0.f : ex2_approx(sm_m[r] - M[mt][x]);
+                        L[mt][x] += f[x] * sm_l[r];
+                    }
+#pragma unroll
+                    for (int i = 0; i < NF; i++) {
+                        const float4 v = merge[(((w & 1) * MT + mt) * (D / 8) + warp * NF + i) * 32 + lane];
+                        acc[mt][i][0] += f[0] * v.x;
+                        acc[mt][i][1] += f[0] * v.y;
+                        acc[mt][i][2] += f[1] * v.z;
+                        acc[mt][i][3] += f[1] * v.w;
+                    }
+                }
+            }
+            __syncthreads();
         }
-        if (item_end) {
-            if (j + 1 < n) next_item<R, UK>(p, piece.pb, c, n_seq);
+        fresh = true;
+
+        // The item's units are [u_item, u_item + nt); one that is not all in this piece leaves a part.
+        const int u_item = piece.u0 + j - unit;
+        const bool begins = ITEMS || u_item >= piece.u0;
+        const bool whole = ITEMS || (begins && u_item + it.nt <= piece.u1);
+        const int slot = (2 * static_cast<int>(blockIdx.x) + (begins ? 1 : 0)) * R;
+        RowInfo ri{0, 0, 0, 0};
+        if (!whole && begins)
+            ri = RowInfo{p.part_row0 + slot, p.part_row0 + slot + R,
+                         cta_of(piece, u_item + it.nt - 1) - static_cast<int>(blockIdx.x) + 1, 2 * R};
+        // columns col + 8 i, + 1 of row r; `first` where the row's sum and its entry are to be written too
+        auto write = [&](auto n_const, int r, int col, auto& v, float m, float l, bool first) {
+            constexpr int N = decltype(n_const)::value;
+            const int rr = it.rb * R + r;
+            const int i_tok = div_group(p, rr);
+            const int64_t t = it.first + i_tok;
+            const int hq = it.h * p.group + rr - i_tok * p.group;
+            const int64_t at = t * p.Hq + hq;
+            if (whole && p.acc == nullptr) {
+                if (p.pre_acc != nullptr) {  // add the row's part over the prefix
+                    const float2 ml = p.pre_ml[at];
+                    const float mn = fmaxf(m, ml.x);
+                    const float fo = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+                    const float fn = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
+#pragma unroll
+                    for (int i = 0; i < N; i++) {
+                        const float2 w = *reinterpret_cast<const float2*>(p.pre_acc + at * D + col + i * 8);
+                        v[i][0] = v[i][0] * fo + w.x * fn;
+                        v[i][1] = v[i][1] * fo + w.y * fn;
+                    }
+                    l = l * fo + ml.y * fn;
+                    m = mn;
+                }
+                const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
+                __nv_bfloat16* dst = p.o + t * p.o_token + hq * p.o_head + col;
+#pragma unroll
+                for (int i = 0; i < N; i++)
+                    *reinterpret_cast<uint32_t*>(dst + i * 8) = pack_bf16x2(v[i][0] * inv, v[i][1] * inv);
+                if (first) p.lse[at] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
+            } else {
+                float* dst = (whole ? p.acc + at * D : p.part_o + static_cast<int64_t>(slot + r) * D) + col;
+#pragma unroll
+                for (int i = 0; i < N; i++) *reinterpret_cast<float2*>(dst + i * 8) = make_float2(v[i][0], v[i][1]);
+                if (first) (whole ? p.acc_ml[at] : p.part_ml[slot + r]) = make_float2(m, l);
+            }
+            if (first && p.info != nullptr && begins)
+                p.info[at] = RowInfo{ri.first + (whole ? 0 : r), ri.second + (whole ? 0 : r), ri.n, ri.stride};
+        };
+        if (ITEMS && CL > 1) {
+            // ---- add the CTAs of the cluster.  Of the item's F column pairs of two rows (in the order of the mma
+            // tiles' lanes) CTA k takes those from k F / CL on: all send theirs to its shared memory, with the
+            // rows' maxima and sums, and after one barrier it adds what came.
+            constexpr int F = MT * (D / 8) * 32;
+            const int shift = 31 - __clz(F) + 1 - __ffs(CL), share = 1 << shift;  // F / CL: both are powers of two
+            float2* got_ml = reinterpret_cast<float2*>(merge + F);  // [CL][R]
+            cluster_arrive();
+            cluster_wait();  // every CTA has added its warps: their buffer is free for what comes
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+                for (int i = 0; i < NF; i++) {
+                    const int f = (mt * (D / 8) + warp * NF + i) * 32 + lane;
+                    cluster_st4(smem_addr(merge + rank * share + (f & (share - 1))), f >> shift,
+                                make_float4(acc[mt][i][0], acc[mt][i][1], acc[mt][i][2], acc[mt][i][3]));
+                }
+#pragma unroll
+                for (int x = 0; x < 2; x++)  // lane 4 rq + c of warp w: to CTA w + 4 (c & 1)
+                    if (warp + 4 * (lane & 1) < CL && (lane & 3) < 2)
+                        cluster_st2(smem_addr(got_ml + rank * R + mt * 16 + rq + 8 * x), warp + 4 * (lane & 1),
+                                    make_float2(M[mt][x], L[mt][x]));
+            }
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+            if (p.pre_acc != nullptr) wait_previous_kernel();
+#pragma unroll 1
+            for (int f0 = tid; f0 < share; f0 += C::kThreads) {
+                const int f = rank * share + f0;
+                const int r = f / ((D / 8) * 32) * 16 + f % 32 / 4, col = f / 32 % (D / 8) * 8 + f % 4 * 2;
+                float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, v[2][1][2] = {{{0.f, 0.f}}, {{0.f, 0.f}}};
+#pragma unroll 4
+                for (int k = 0; k < CL; k++)
+#pragma unroll
+                    for (int x = 0; x < 2; x++) m[x] = fmaxf(m[x], got_ml[k * R + r + 8 * x].x);
+#pragma unroll 4
+                for (int k = 0; k < CL; k++) {
+                    const float4 a = merge[k * share + f0];
+                    const float2 m0 = got_ml[k * R + r], m1 = got_ml[k * R + r + 8];
+                    const float w0 = m0.x == -INFINITY ? 0.f : ex2_approx(m0.x - m[0]);
+                    const float w1 = m1.x == -INFINITY ? 0.f : ex2_approx(m1.x - m[1]);
+                    v[0][0][0] += w0 * a.x;
+                    v[0][0][1] += w0 * a.y;
+                    v[1][0][0] += w1 * a.z;
+                    v[1][0][1] += w1 * a.w;
+                    l[0] += w0 * m0.y;
+                    l[1] += w1 * m1.y;
+                }
+#pragma unroll 1
+                for (int x = 0; x < 2; x++) {
+                    const bool hi = x;
+                    float u[1][2] = {{hi ? v[1][0][0] : v[0][0][0], hi ? v[1][0][1] : v[0][0][1]}};
+                    if (r + 8 * x < rows_left)
+                        write(std::integral_constant<int, 1>{}, r + 8 * x, col, u, hi ? m[1] : m[0], hi ? l[1] : l[0],
+                              col == 0);
+                }
+            }
+            if (j + 1 < issued) __syncthreads();  // read, before the next item's warps write there
         } else {
-            c.i++;
+            if (p.pre_acc != nullptr) wait_previous_kernel();
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                for (int x = 0; x < 2; x++) {
+                    const int r = mt * 16 + rq + 8 * x;
+                    if (r >= rows_left) continue;
+                    float v[NF][2];
+#pragma unroll
+                    for (int i = 0; i < NF; i++) {
+                        v[i][0] = acc[mt][i][2 * x];
+                        v[i][1] = acc[mt][i][2 * x + 1];
+                    }
+                    write(std::integral_constant<int, NF>{}, r, warp * (D / 4) + cq, v, M[mt][x], L[mt][x],
+                          warp == 0 && lane % 4 == 0);
+                }
         }
     }
     if (dead) {
         // copies still in flight land before the CTA's memory goes away
-        for (int j = max(issued - ST, 0); j < issued; j++) mbar_wait(&bar[j % ST], (j / ST) & 1, p.timeout);
+        for (int j = max(live - ST, 0); j < live; j++) mbar_wait(&bar[j % ST], (j / ST) & 1, p.timeout);
     }
     wait_previous_kernel();
 }

@@ -38,7 +38,7 @@ namespace sa {
 // Where a row's result lies (one per row and query head): in n > 0 parts at rows
 // `first`, `second`, `second` + stride, ... of the part arrays, or, n = 0,
 // finished by its CTA.
-struct RowInfo {
+struct alignas(16) RowInfo {
     int32_t first, second, n, stride;
 };
 
@@ -53,6 +53,7 @@ struct PassParams {
     const int32_t* table;      // [B, max_pages]; over the prefix: its pages
     int64_t table_stride;
     int32_t B, T, Hq, Hkv, group;
+    uint32_t group_mul, group_shift;  // x / group = x * group_mul >> group_shift for 0 <= x < 2^31
     int32_t n_pages, page_shift, max_pages;
     int32_t prefix_len;        // tokens before a sequence's own
     int32_t over_prefix;       // 1: all rows against the prefix; 0: each sequence against its own tokens
@@ -63,9 +64,11 @@ struct PassParams {
     float* part_o;             // [2 * CTAs * R, D] parts of cut items (this pass's)
     float2* part_ml;           // [2 * CTAs * R] running maximum (log2 units), sum
     int32_t part_row0;         // index of the first of them in the arrays that join_kernel reads
-    RowInfo* info;             // [T, Hq]
+    RowInfo* info;             // [T, Hq]; null where no row is read from parts
     float* acc;                // null: finished rows go to o and lse; else [T, Hq, D] unnormalised,
     float2* acc_ml;            // [T, Hq]
+    const float* pre_acc;      // not null: what the pass over the prefix left, added to every row
+    const float2* pre_ml;
     int32_t* status;
     long long timeout;
     int32_t debug_flags;
@@ -103,6 +106,11 @@ __device__ __forceinline__ SeqView load_seq(const PassParams& p, int b)
         s.p0 = s.len - s.m;
     }
     return s;
+}
+
+__device__ __forceinline__ int div_group(const PassParams& p, int x)
+{
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(x)) * p.group_mul >> p.group_shift);
 }
 
 // Does the pass take a sequence of this many rows?
@@ -152,7 +160,7 @@ __device__ __forceinline__ Units item_units(const PassParams& p, const PassBound
     const int r0 = rb * R;
     const int r1 = min(r0 + R, s.m * p.group) - 1;
     const int base = p.prefix_len + s.p0;
-    return units_of(p, base + r0 / p.group, base + r1 / p.group, s.len, UK);
+    return units_of(p, base + div_group(p, r0), base + div_group(p, r1), s.len, UK);
 }
 
 // Position of a token (prefix included), for a pass over the prefix: the sequence
@@ -196,134 +204,129 @@ __device__ __forceinline__ void next_item(const PassParams& p, const PassBounds&
     c.u = item_units<R, UK>(p, pb, c.s, c.rb);
 }
 
-// The piece of the line that this CTA takes: [u0, u1) of U units, G CTAs with
-// work.  Called by all NT threads; `sh` holds NT / 32 + 4 int64 in shared memory.
+// The piece of the line that this CTA takes: [u0, u1) of U units (or items: ITEMS),
+// cut into G equal pieces.  The host has checked that U stays below 2^31.
 struct Piece {
-    int64_t U, u0, u1;
+    int U, u0, u1;
+    int each, more;  // units of a piece; the first `more` pieces have one more
     int G;
     PassBounds pb;
-    Cursor c;  // at u0 (valid when u0 < u1)
+    Cursor c;        // at u0 (valid when u0 < u1)
 };
 
-template <int R, int UK>
-__device__ __forceinline__ int64_t seq_units(const PassParams& p, const PassBounds& pb, const SeqView& s)
+template <int R, int UK, bool ITEMS>
+__device__ __forceinline__ int seq_units(const PassParams& p, const PassBounds& pb, const SeqView& s)
 {
     const int rows = s.m * p.group;
     if (rows == 0 || !takes(p, rows)) return 0;
     const int nrb = (rows + R - 1) / R;
-    int64_t n = 0;
-    if (p.over_prefix) {
-        n = static_cast<int64_t>(nrb) * item_units<R, UK>(p, pb, s, 0).nt;
-    } else {
+    int n = nrb;
+    if (!ITEMS && p.over_prefix) n = nrb * item_units<R, UK>(p, pb, s, 0).nt;
+    if (!ITEMS && !p.over_prefix) {
+        n = 0;
+#pragma unroll 1
         for (int rb = 0; rb < nrb; rb++) n += item_units<R, UK>(p, pb, s, rb).nt;
     }
     return n * p.Hkv;
 }
 
-template <int R, int UK, int NT>
-__device__ __forceinline__ Piece find_piece(const PassParams& p, int min_units, int64_t* sh)
+// The sequence that find_piece looks at first in this lane.
+__device__ __forceinline__ SeqView peek_seq(const PassParams& p)
 {
-    constexpr int NWARP = NT / 32;
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int n_seq = p.over_prefix ? 1 : p.B;
+    return load_seq(p, min(static_cast<int>(threadIdx.x % 32) * ((n_seq + 31) / 32), n_seq - 1));
+}
+
+// Find the piece that `cta` of n_cta takes (`ahead`: from peek_seq).  By a whole warp, on its own (no barrier: each
+// warp of a CTA finds the same).  It is the first thing every CTA does, and its code runs
+// once: it is kept short, since instructions come from L2 the first time.
+template <int R, int UK, bool ITEMS>
+__device__ __forceinline__ Piece find_piece(const PassParams& p, const SeqView& ahead, int cta, int n_cta)
+{
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int lane = threadIdx.x % 32;
     Piece r;
     r.pb = PassBounds{0, 0};
     const int n_seq = p.over_prefix ? 1 : p.B;
     if (p.over_prefix) {
-        // the rows' positions: the nearest and the farthest of all sequences
+        // the rows' positions: the lowest and the highest of all sequences
         int lo = INT32_MAX, hi = INT32_MIN;
-        for (int b = tid; b < p.B; b += NT) {
+#pragma unroll 1
+        for (int b = lane; b < p.B; b += 32) {
             const int m = __ldg(&p.q_start[b + 1]) - __ldg(&p.q_start[b]);
-            if (m <= 0) continue;
             const int last = p.prefix_len + cached_len(p, b) - 1;
+            if (m <= 0) continue;
             lo = min(lo, last - m + 1);
             hi = max(hi, last);
         }
-        for (int o = 16; o; o >>= 1) {
-            lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-        if (lane == 0) sh[warp] = lo;
-        __syncthreads();
-        for (int w = 0; w < NWARP; w++) lo = min(lo, static_cast<int>(sh[w]));
-        __syncthreads();
-        if (lane == 0) sh[warp] = hi;
-        __syncthreads();
-        for (int w = 0; w < NWARP; w++) hi = max(hi, static_cast<int>(sh[w]));
-        __syncthreads();
-        r.pb = PassBounds{lo, hi};
+        r.pb = PassBounds{__reduce_min_sync(kAll, lo), __reduce_max_sync(kAll, hi)};
     }
-    // units of this thread's sequences, and of those before them
-    const int per = (n_seq + NT - 1) / NT;
-    const int b0 = min(tid * per, n_seq), b1 = min(b0 + per, n_seq);
-    int64_t own = 0;
-    for (int b = b0; b < b1; b++) own += seq_units<R, UK>(p, r.pb, load_seq(p, b));
-    int64_t incl = own;
+    // units of this lane's sequences, and of those before them
+    const int per = (n_seq + 31) / 32;
+    const int b0 = lane * per, b1 = min(b0 + per, n_seq);
+    int own = 0;
+    SeqView s = ahead;
+#pragma unroll 1
+    for (int b = b0; b < b1;) {
+        own += seq_units<R, UK, ITEMS>(p, r.pb, s);
+        if (++b < b1) s = load_seq(p, b);
+    }
+    int incl = own;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        const int y = __shfl_up_sync(kAll, incl, o);
         if (lane >= o) incl += y;
     }
-    if (lane == 31) sh[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - own, U = 0;
-    for (int w = 0; w < NWARP; w++) {
-        if (w < warp) before += sh[w];
-        U += sh[w];
-    }
-    r.U = U;
-    // as many CTAs as get min_units units each
-    int64_t G = (U + min_units - 1) / min_units;
-    G = min(G, static_cast<int64_t>(gridDim.x));
-    r.G = static_cast<int>(G);
-    const int64_t c = blockIdx.x;
+    r.U = __shfl_sync(kAll, incl, 31);
+    r.G = min(r.U, n_cta);
     r.u0 = r.u1 = 0;
-    if (c < G) {
-        r.u0 = c * U / G;
-        r.u1 = (c + 1) * U / G;
-    }
-    int* found = reinterpret_cast<int*>(sh + NWARP);  // b, units before it (2 words)
-    if (r.u0 < r.u1 && before <= r.u0 && r.u0 < before + own) {
-        int64_t at = before;
-        for (int b = b0; b < b1; b++) {
-            const int64_t n = seq_units<R, UK>(p, r.pb, load_seq(p, b));
-            if (r.u0 < at + n) {
-                found[0] = b;
-                sh[NWARP + 1] = at;
-                break;
-            }
-            at += n;
-        }
-    }
-    __syncthreads();
-    if (r.u0 < r.u1) {
-        r.c.b = found[0];
-        int64_t at = sh[NWARP + 1];
-        r.c.s = load_seq(p, r.c.b);
-        r.c.rb = 0;
-        for (;;) {
-            r.c.u = item_units<R, UK>(p, r.pb, r.c.s, r.c.rb);
-            const int64_t n = static_cast<int64_t>(r.c.u.nt) * p.Hkv;
+    if (cta >= r.G) return r;
+    r.each = static_cast<uint32_t>(r.U) / static_cast<uint32_t>(r.G);
+    r.more = r.U - r.each * r.G;
+    r.u0 = cta * r.each + min(cta, r.more);
+    r.u1 = r.u0 + r.each + (cta < r.more ? 1 : 0);
+    int at = incl - own;
+    const bool here = at <= r.u0 && r.u0 < incl;
+    const int who = __ffs(__ballot_sync(kAll, here)) - 1;
+    int b = b0;
+    if (per > 1 && here) {
+#pragma unroll 1
+        for (;; b++) {
+            const int n = seq_units<R, UK, ITEMS>(p, r.pb, load_seq(p, b));
             if (r.u0 < at + n) break;
             at += n;
-            r.c.rb++;
         }
-        const int rest = static_cast<int>(r.u0 - at);
-        r.c.h = rest / r.c.u.nt;
-        r.c.i = rest % r.c.u.nt;
     }
+    r.c.b = __shfl_sync(kAll, b, who);
+    at = __shfl_sync(kAll, at, who);
+    r.c.s = load_seq(p, r.c.b);
+    r.c.rb = 0;
+#pragma unroll 1
+    for (;; r.c.rb++) {
+        r.c.u = item_units<R, UK>(p, r.pb, r.c.s, r.c.rb);
+        const int n = (ITEMS ? 1 : r.c.u.nt) * p.Hkv;
+        if (r.u0 < at + n) break;
+        at += n;
+    }
+    const uint32_t rest = r.u0 - at;
+    r.c.h = ITEMS ? rest : rest / static_cast<uint32_t>(r.c.u.nt);
+    r.c.i = ITEMS ? 0 : rest - r.c.h * r.c.u.nt;
     return r;
 }
 
 // CTA whose piece holds unit u.
-__device__ __forceinline__ int cta_of(const Piece& r, int64_t u)
+__device__ __forceinline__ int cta_of(const Piece& r, int u)
 {
-    return static_cast<int>(((u + 1) * r.G + r.U - 1) / r.U) - 1;
+    const int longer = r.more * (r.each + 1);
+    return u < longer ? static_cast<uint32_t>(u) / static_cast<uint32_t>(r.each + 1)
+                      : r.more + static_cast<uint32_t>(u - longer) / static_cast<uint32_t>(r.each);
 }
 
 // Page of key k (k below the sequence's length), or a page past the cache's end
 // (which the tensor map fills with zeros) where the table names none of its pages.
-__device__ __forceinline__ int page_of(const PassParams& p, const Cursor& c, int k)
+__device__ __forceinline__ int page_of(const PassParams& p, int b, int k)
 {
-    const int pg = __ldg(&p.table[static_cast<int64_t>(c.b) * p.table_stride + (k >> p.page_shift)]);
+    const int pg = __ldg(&p.table[static_cast<int64_t>(b) * p.table_stride + (k >> p.page_shift)]);
     return pg >= 0 && pg < p.n_pages ? pg : p.n_pages;
 }
 
@@ -365,7 +368,7 @@ struct JoinParams {
 // the parts.  WPR warps share a row (each takes every WPR-th part, then they are
 // added in the order of the warps): one where rows are many, eight where a few
 // rows have up to a part per CTA, whose loads are then in flight together.
-template <int D, int WPR, bool PREFIX>
+template <int D, int WPR, int kGroup, bool PREFIX>
 __global__ void __launch_bounds__(256) join_kernel(const JoinParams p)
 {
     constexpr int kRows = 8 / WPR;
@@ -376,36 +379,54 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p)
     __shared__ float sh_o[8][D];
     __shared__ float sh_m[8], sh_l[8];
     const int64_t total = static_cast<int64_t>(min(max(__ldg(&p.q_start[p.B]), 0), p.T)) * p.Hq;
-    // every warp of a block makes the same number of rounds
-    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < total;
-         row0 += static_cast<int64_t>(gridDim.x) * kRows) {
-        const int64_t row = row0 + warp / WPR;
-        const bool have = row < total;
-        float acc[E];
-#pragma unroll
-        for (int e = 0; e < E; e++) acc[e] = 0.f;
-        float M = -INFINITY, L = 0.f;
-        bool write = PREFIX;
-        auto add = [&](const float* src, float2 ml) {
-            if (ml.x == -INFINITY) return;
-            const float mn = fmaxf(M, ml.x);
-            const float a = ex2_approx(M - mn), b = ex2_approx(ml.x - mn);
-#pragma unroll
-            for (int e = 0; e < E; e++) acc[e] = acc[e] * a + src[e] * b;
-            L = L * a + ml.y * b;
-            M = mn;
-        };
-        if (have) {
+    // A warp looks at kGroup rows at once (most rows may be finished already) and takes them one by one; where
+    // warps share a row, every warp of a block makes the same number of rounds.
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows * kGroup; row0 < total;
+         row0 += static_cast<int64_t>(gridDim.x) * kRows * kGroup) {
+        const int64_t base = row0 + warp / WPR * kGroup;
+        RowInfo ris[2] = {{-1, 0, 0, 0}, {-1, 0, 0, 0}};
+        bool todo = false;
+        if (lane < kGroup && base + lane < total) {
 #pragma unroll
             for (int s = 0; s < (PREFIX ? 2 : 1); s++) {
-                RowInfo ri = p.info[s][row];
+                RowInfo ri = p.info[s][base + lane];
                 // a row that no sequence covers (q_start not ascending from 0) has no entry: nothing of it
                 // is followed
                 if (ri.n < 0 || ri.n > p.part_rows || ri.stride < 0 || ri.stride > p.part_rows || ri.first < 0 ||
                     ri.second < 0 ||
                     (ri.n > 0 && (ri.first >= p.part_rows ||
                                   ri.second + static_cast<int64_t>(ri.n - 2) * ri.stride >= p.part_rows)))
-                    continue;
+                    ri.n = -1;
+                ris[s] = ri;
+                todo = todo || PREFIX || ri.n > 0;
+            }
+        }
+        for (uint32_t mask = __ballot_sync(0xffffffffu, todo), r = 0; WPR > 1 ? r == 0 : mask != 0; r++) {
+            const int src = WPR > 1 ? 0 : __ffs(mask) - 1;
+            const bool write = WPR > 1 ? mask != 0 : true;
+            mask &= mask - 1;
+            const int64_t row = base + src;
+            float acc[E];
+#pragma unroll
+            for (int e = 0; e < E; e++) acc[e] = 0.f;
+            float M = -INFINITY, L = 0.f;
+            auto add = [&](const float* v, float2 ml) {
+                if (ml.x == -INFINITY) return;
+                const float mn = fmaxf(M, ml.x);
+                const float a = ex2_approx(M - mn), b = ex2_approx(ml.x - mn);
+#pragma unroll
+                for (int e = 0; e < E; e++) acc[e] = acc[e] * a + v[e] * b;
+                L = L * a + ml.y * b;
+                M = mn;
+            };
+#pragma unroll
+            for (int s = 0; s < (PREFIX ? 2 : 1); s++) {
+                RowInfo ri;
+                ri.first = __shfl_sync(0xffffffffu, ris[s].first, src);
+                ri.second = __shfl_sync(0xffffffffu, ris[s].second, src);
+                ri.n = __shfl_sync(0xffffffffu, ris[s].n, src);
+                ri.stride = __shfl_sync(0xffffffffu, ris[s].stride, src);
+                if (!write) continue;
                 if (ri.n == 0) {
                     if (PREFIX && sub == 0) {
                         float v[E];
@@ -415,7 +436,6 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p)
                     }
                     continue;
                 }
-                write = true;
                 constexpr int K = 4;  // parts in flight
                 for (int k0 = sub; k0 < ri.n; k0 += K * WPR) {
                     float v[K][E];
@@ -434,35 +454,35 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p)
                     for (int j = 0; j < K; j++) add(v[j], ml[j]);
                 }
             }
-        }
-        if constexpr (WPR > 1) {
+            if constexpr (WPR > 1) {
 #pragma unroll
-            for (int e = 0; e < E; e++) sh_o[warp][lane * E + e] = acc[e];
-            if (lane == 0) {
-                sh_m[warp] = M;
-                sh_l[warp] = L;
-            }
-            __syncthreads();
-            if (sub == 0) {
-                for (int w = 1; w < WPR; w++) {
-                    float v[E];
-#pragma unroll
-                    for (int e = 0; e < E; e++) v[e] = sh_o[warp + w][lane * E + e];
-                    add(v, make_float2(sh_m[warp + w], sh_l[warp + w]));
+                for (int e = 0; e < E; e++) sh_o[warp][lane * E + e] = acc[e];
+                if (lane == 0) {
+                    sh_m[warp] = M;
+                    sh_l[warp] = L;
                 }
+                __syncthreads();
+                if (sub == 0) {
+                    for (int w = 1; w < WPR; w++) {
+                        float v[E];
+#pragma unroll
+                        for (int e = 0; e < E; e++) v[e] = sh_o[warp + w][lane * E + e];
+                        add(v, make_float2(sh_m[warp + w], sh_l[warp + w]));
+                    }
+                }
+                __syncthreads();
             }
-            __syncthreads();
-        }
-        if (have && write && sub == 0) {
-            const float inv = L > 0.f ? 1.f / L : 0.f;
-            const int t = static_cast<int>(row / p.Hq), h = static_cast<int>(row % p.Hq);
-            __nv_bfloat16* dst = p.o + t * p.o_token + h * p.o_head + lane * E;
-            if constexpr (E == 4)
-                *reinterpret_cast<uint2*>(dst) =
-                    make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-            else
-                *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-            if (lane == 0) p.lse[row] = L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+            if (write && sub == 0) {
+                const float inv = L > 0.f ? 1.f / L : 0.f;
+                const uint32_t t = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.Hq), h = static_cast<uint32_t>(row) - t * p.Hq;
+                __nv_bfloat16* dst = p.o + t * p.o_token + h * p.o_head + lane * E;
+                if constexpr (E == 4)
+                    *reinterpret_cast<uint2*>(dst) =
+                        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+                else
+                    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+                if (lane == 0) p.lse[row] = L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+            }
         }
     }
 }

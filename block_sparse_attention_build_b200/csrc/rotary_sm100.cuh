@@ -173,6 +173,18 @@ __global__ void __launch_bounds__(kRotThreads, rot_blocks(LAYOUT)) rotary_kernel
         sh_axis[i] = spec.axis[i];
     }
     __syncthreads();
+    constexpr int U = rot_unroll(LAYOUT);
+    const int h_begin = static_cast<int>(blockIdx.y) * p.heads_per, h_end = h_begin + p.heads_per;
+    if constexpr (PAGED) {
+        // finding the token's sequence, position and page takes several loads one after another: have the
+        // first rows on their way to L2 meanwhile
+        if (t < p.rows) {
+            const __nv_bfloat16* q = p.q.p + t * p.q.token + item * (D / kItems);
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                if (h_begin + u < p.Hq) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + (h_begin + u) * p.q.head));
+        }
+    }
 
     // where the token stands, and where its key and value go
     bool have;  // lanes without a token stay: others may shuffle with them
@@ -274,8 +286,6 @@ __global__ void __launch_bounds__(kRotThreads, rot_blocks(LAYOUT)) rotary_kernel
         }
     };
 
-    constexpr int U = rot_unroll(LAYOUT);
-    const int h_begin = static_cast<int>(blockIdx.y) * p.heads_per, h_end = h_begin + p.heads_per;
     int first = 0;  // heads before this kind's
 #pragma unroll 1
     for (int kind = 0; kind < (PAGED ? 3 : 2); kind++) {  // queries, keys, values (copied)
