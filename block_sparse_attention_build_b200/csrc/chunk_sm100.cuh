@@ -7,17 +7,22 @@
 // is 4 * 256 * 128 * D operations on 512 D bytes: the tensor cores and the
 // exponentials bound it, not memory.
 //
-// Warp roles (384 threads, three warpgroups):
-//   warp 0     producer: K and V tiles of the CTA's units through one ring of
-//              stages, a page (or 128 places of one) per TMA, its lanes side by side
-//   warp 1     allocates tensor memory; one lane issues every tcgen05.mma
-//   warps 2, 3 Q of slot A, slot B: rows lie where tokens and heads put them, so
-//              they are gathered with cp.async into the swizzled layout that TMA
-//              would write, while the previous item's last softmax and PV still run
-//   warps 4-7  softmax of slot A, warps 8-11 of slot B: a thread per row
+// Warp roles (384 threads, three warpgroups, with fwd_kernel's register split):
+//   warp 0      producer: walks the CTA's items, describes each segment (the units
+//               of an item in this CTA's piece) in a two-entry ring that the other
+//               roles read, and loads K and V tiles through one ring of stages, a
+//               page (or 128 places of one) per TMA, its lanes side by side
+//   warp 1      allocates tensor memory; one lane issues every tcgen05.mma
+//   warps 2, 3  Q of slot A, slot B: rows lie where tokens and heads put them, so
+//               they are gathered with cp.async into the swizzled layout that TMA
+//               would write, while the previous item's last softmax and PV still run
+//   warps 4-7   softmax of slot A, warps 8-11 of slot B: a thread per row
 //
-// Order of the tensor cores: PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).  Tensor memory
-// (512 columns): S_A, S_B (128 each; P over their first half), O_A, O_B (D each).
+// Order of the tensor cores: PV_A(j), S_A(j+1), PV_B(j), S_B(j+1), 512 cycles each
+// at D = 128.  Tensor memory (512 columns): S_A, S_B (128 each; P over their first
+// half), O_A, O_B (D each).  Two threads to a row (half of the keys each, the row's
+// maximum exchanged) were slower: 2190 us against 2060 for 4096 new tokens behind
+// 28672, 32/8 heads of 128, where the board runs at its 1000 W limit.
 // Places no row sees may hold anything: scores there are replaced, and slot A's
 // threads clear the tile's V rows before P V (0 x infinity is not 0).
 //
@@ -30,6 +35,21 @@
 
 namespace sa {
 
+// One segment, as the producer describes it.
+struct Segment {
+    int32_t n;                 // units here; 0: no more segments
+    int32_t i, ns, bs, hi;     // first of them, and where units and keys lie (see Units)
+    int32_t first, rows, rb, h, base;  // item: first token, its rows, row block, head, position of the first token
+    int32_t begins, whole;     // the item's first unit is here; all of them are
+    int32_t parts;             // CTAs that share it (where it begins)
+    int32_t pad[3];
+    __device__ __forceinline__ int key(int j) const
+    {
+        const int u = i + j;
+        return (u < ns ? u : bs + (u - ns)) * 128;
+    }
+};
+
 template <int D>
 struct ChunkCfg {
     static constexpr int kThreads = 384;
@@ -40,8 +60,9 @@ struct ChunkCfg {
     static constexpr int kPanel = 128 * 128;                 // 64 columns x 128 rows
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kOffRing = 2 * kQBytes;
-    static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
-    static constexpr int kNumBars = 2 * kStages + 2 * 6 + 1;
+    static constexpr int kOffSeg = kOffRing + kStages * kTileBytes;
+    static constexpr int kOffBar = kOffSeg + 2 * static_cast<int>(sizeof(Segment));
+    static constexpr int kNumBars = 2 * kStages + 2 * 6 + 2 * 2 + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kSmemUsed = kOffMisc + 16;
     // at least this much, so that one CTA owns the SM's tensor memory
@@ -66,20 +87,25 @@ __global__ void __launch_bounds__(384, 1)
     extern __shared__ __align__(1024) uint8_t smem[];  // swizzled tiles sit on 1024 bytes
     uint8_t* sQ = smem;
     uint8_t* ring = smem + C::kOffRing;
+    Segment* segs_ring = reinterpret_cast<Segment*>(smem + C::kOffSeg);
     uint64_t* ring_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [S]
     uint64_t* ring_empty = ring_full + S;                                  // [S]
-    uint64_t* q_full = ring_empty + S;   // [2]
-    uint64_t* q_empty = q_full + 2;      // [2] the slot's last S MMA of the item is done
-    uint64_t* s_full = q_empty + 2;      // [2]
-    uint64_t* p_full = s_full + 2;       // [2]
-    uint64_t* o_full = p_full + 2;       // [2]
-    uint64_t* o_empty = o_full + 2;      // [2]
-    uint64_t* drain = o_empty + 2;       // [1]
+    uint64_t* q_full = ring_empty + S;     // [2]
+    uint64_t* q_empty = q_full + 2;        // [2] the slot's last S MMA of the item is done
+    uint64_t* s_full = q_empty + 2;        // [2]
+    uint64_t* p_full = s_full + 2;         // [2]
+    uint64_t* o_full = p_full + 2;         // [2]
+    uint64_t* o_empty = o_full + 2;        // [2]
+    uint64_t* info_full = o_empty + 2;     // [2] a segment is described
+    uint64_t* info_empty = info_full + 2;  // [2] all roles are done with it
+    uint64_t* drain = info_empty + 2;      // [1]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
 
+    launch_dependents();
+    if (p.tails != nullptr && threadIdx.x < R) p.tails[blockIdx.x * R + threadIdx.x] = TailRow{0, 0};
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; i++) {
             mbar_init(&ring_full[i], 1);
@@ -89,9 +115,11 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&q_full[x], 32);
             mbar_init(&q_empty[x], 1);
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[x], 128);
+            mbar_init(&p_full[x], 4);    // a lane of each softmax warp of the slot
             mbar_init(&o_full[x], 1);
-            mbar_init(&o_empty[x], 128);
+            mbar_init(&o_empty[x], 4);
+            mbar_init(&info_full[x], 1);
+            mbar_init(&info_empty[x], 1 + 2 + 8);  // a lane of the MMA, Q and softmax warps
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -101,32 +129,30 @@ __global__ void __launch_bounds__(384, 1)
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
     }
-    if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-    }
-    launch_dependents();
-    const Piece piece = find_piece<R, UK, false>(p, peek_seq(p), blockIdx.x, gridDim.x);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const long long lim = p.timeout;
-    const int n_seq = p.over_prefix ? 1 : p.B;
-    const int total = piece.u1 - piece.u0;
     auto fail = [&]() {
         *abort_flag = 1;
         atomicOr(p.status, ST_PAGED_WAIT);
     };
-    // The CTA's segments: for each, the item and the units [c.i, c.i + n) of it.
-    Cursor c = piece.c;
-    int left = total;
-    auto seg_len = [&]() { return min(c.u.nt - c.i, left); };
-    auto seg_next = [&](int n) {
-        left -= n;
-        if (left > 0) next_item<R, UK>(p, piece.pb, c, n_seq);
+    // every lane polls; the outcome is made warp-uniform
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim) && !*abort_flag);
     };
-    auto rows_of_item = [&]() { return min(c.s.m * p.group - c.rb * R, R); };
+    // The next segment (k-th): false at the end or when a wait ran out.
+    bool ok = true;
+    auto open_segment = [&](int k) -> const Segment* {
+        const Segment* g = &segs_ring[k & 1];
+        ok = wait(&info_full[k & 1], (k >> 1) & 1);
+        return ok && g->n > 0 ? g : nullptr;
+    };
+    auto close_segment = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&info_empty[k & 1]);
+    };
     // warp-uniform warpgroup index, so that the register split applies per branch
     const int wg = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 128, 0);
 
@@ -134,46 +160,72 @@ __global__ void __launch_bounds__(384, 1)
         regs_dec<kRegsControl>();
         if (warp == 0) {
             // ============================================================ producer
+            const Piece piece = find_piece<R, UK, false>(p, peek_seq(p), blockIdx.x, gridDim.x);
+            const int n_seq = p.over_prefix ? 1 : p.B;
             const int page_rows = min(1 << p.page_shift, UK);
             constexpr int P = D / 64;  // column panels
-            int pos = 0;
-            bool dead = false;
-            auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-                return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim));
-            };
-            while (left > 0 && !dead) {
-                const int n = seg_len();
-                for (int j = 0; j < n && !dead; j++) {
-                    const int k0 = c.u.key(c.i + j, UK);
-                    // boxes that begin below the item's last key, a panel each
-                    const int nb = min(max((c.u.hi - k0 + page_rows - 1) / page_rows, 0), UK / page_rows);
-                    const int box = lane / P, panel = lane % P;
-                    const bool mine = box < nb;
-                    const int k = k0 + box * page_rows;
-                    const int pg = mine ? page_of(p, c.b, k) : 0;
-                    const int row = k & ((1 << p.page_shift) - 1);
-#pragma unroll
+            const int box = lane / P, panel = lane % P;
+            Cursor c = piece.c;
+            int left = piece.u1 - piece.u0;
+            int pos = 0, k_seg = 0;
+            for (;; k_seg++) {
+                // describe the segment
+                if (!(ok = wait(&info_empty[k_seg & 1], ((k_seg >> 1) & 1) ^ 1))) break;
+                const int n = left > 0 ? min(c.u.nt - c.i, left) : 0;
+                if (lane == 0) {
+                    Segment& g = segs_ring[k_seg & 1];
+                    g.n = n;
+                    if (n > 0) {
+                        const int u_item = piece.u1 - left - c.i;
+                        g.i = c.i;
+                        g.ns = c.u.ns;
+                        g.bs = c.u.bs;
+                        g.hi = c.u.hi;
+                        g.first = c.s.first;
+                        g.rows = min(c.s.m * p.group - c.rb * R, R);
+                        g.rb = c.rb;
+                        g.h = c.h;
+                        g.base = p.prefix_len + c.s.p0;
+                        g.begins = u_item >= piece.u0;
+                        g.whole = u_item >= piece.u0 && u_item + c.u.nt <= piece.u1;
+                        g.parts = 0;
+                        if (g.begins && !g.whole) g.parts = cta_of(piece, u_item + c.u.nt - 1) - static_cast<int>(blockIdx.x) + 1;
+                    }
+                    mbar_arrive(&info_full[k_seg & 1]);
+                }
+                __syncwarp();
+                if (n == 0) break;
+                // the pages of a tile are looked up while the one before it is loaded
+                auto tile_key = [&](int j) { return c.u.key(c.i + j, UK); };
+                auto boxes = [&](int k0) {
+                    return min(max((c.u.hi - k0 + page_rows - 1) / page_rows, 0), UK / page_rows);
+                };
+                auto page_at = [&](int k0) { return box < boxes(k0) ? page_of(p, c.b, k0 + box * page_rows) : 0; };
+                int pg_next = page_at(tile_key(0));
+                for (int j = 0; j < n && ok; j++) {
+                    const int k0 = tile_key(j), nb = boxes(k0), pg = pg_next;
+                    if (j + 1 < n) pg_next = page_at(tile_key(j + 1));
+                    const int row = (k0 + box * page_rows) & ((1 << p.page_shift) - 1);
+#pragma unroll 1
                     for (int v = 0; v < 2; v++) {  // K, then V
-                        if (!wait(&ring_empty[pos % S], ((pos / S) & 1) ^ 1)) {
-                            if (lane == 0) fail();
-                            dead = true;
-                            break;
-                        }
                         const int st = pos % S;
+                        if (!(ok = wait(&ring_empty[st], ((pos / S) & 1) ^ 1))) break;
                         const bool skip = (p.debug_flags & 1) && blockIdx.x == 0 && pos == 0;
                         if (lane == 0) mbar_arrive_expect_tx(&ring_full[st], skip ? 16 : nb * page_rows * D * 2);
                         __syncwarp();
-                        if (mine && !skip)
+                        if (box < nb && !skip)
                             tma_load_5d(ring + st * C::kTileBytes + panel * C::kPanel + box * page_rows * 128,
                                         v == 0 ? &tmK : &tmV, &ring_full[st], 0, row, panel, c.h, pg);
                         __syncwarp();
                         pos++;
                     }
-                    if (__any_sync(0xffffffffu, *abort_flag != 0)) dead = true;
                 }
-                seg_next(n);
+                if (!ok) break;
+                left -= n;
+                if (left > 0) next_item<R, UK>(p, piece.pb, c, n_seq);
             }
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) {
+            if (!ok) {
+                if (lane == 0) fail();
                 // copies still in flight land before the CTA's memory goes away
                 for (int i = pos > S ? pos - S : 0; i < pos; i++) mbar_wait(&ring_full[i % S], (i / S) & 1, lim);
             }
@@ -215,16 +267,15 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 __syncwarp();
             };
-            auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-                return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim));
-            };
             int steps[2] = {0, 0};  // S/P handshakes per slot
             int segs[2] = {0, 0};   // segments per slot (phases of q_full, o_full, o_empty)
             int pos = 0;
-            bool ok = true;
-            while (left > 0 && ok) {
-                const int n = seg_len();
-                const int nx = rows_of_item() > 128 ? 2 : 1;
+            for (int k_seg = 0;; k_seg++) {
+                const Segment* g = open_segment(k_seg);
+                if (!g) break;
+                const int n = g->n;
+                const int nx = g->rows > 128 ? 2 : 1;
+                close_segment(k_seg);
                 ok = wait(&ring_full[pos % S], (pos / S) & 1);
 #pragma unroll
                 for (int x = 0; x < 2; x++) {
@@ -255,148 +306,141 @@ __global__ void __launch_bounds__(384, 1)
                         if (last) {
                             commit(&o_full[x]);
                         } else {
-                            if (x == 0 && !wait(&ring_full[pk % S], (pk / S) & 1)) {
-                                ok = false;
-                                break;
-                            }
+                            if (x == 0 && !(ok = wait(&ring_full[pk % S], (pk / S) & 1))) break;
                             tc_fence_after_sync();
                             issue_s(x, pk % S);
                             commit(&s_full[x]);
                             if (j + 2 == n) commit(&q_empty[x]);  // the slot's last read of Q
                         }
                     }
-                    ok = __all_sync(0xffffffffu, ok && !*abort_flag);
                     if (!ok) break;
                     commit(&ring_empty[pv % S]);
                     if (!last) commit(&ring_empty[pk % S]);
                 }
+                if (!ok) break;
 #pragma unroll
                 for (int x = 0; x < 2; x++)
                     if (x < nx) segs[x]++;
                 pos += 2 * n;
-                seg_next(n);
             }
             if (!ok && lane == 0) fail();
             // all issued tensor-core work is finished before the memory is released
             commit(drain);
-            if (!wait(drain, 0) && lane == 0) atomicOr(p.status, ST_DRAIN_WAIT);
+            if (!__all_sync(0xffffffffu, mbar_wait(drain, 0, lim)) && lane == 0) atomicOr(p.status, ST_DRAIN_WAIT);
         } else {
             // ============================================================ Q of slot x
             const int x = warp - 2;
             constexpr int L = D / 8;        // lanes of a row, 16 bytes each
             constexpr int RW = 32 / L;      // rows of one step
-            const uint32_t dst0 = smem_addr(sQ) + x * C::kQBytes;
+            const int ch = lane % L;
+            const uint32_t dst0 = smem_addr(sQ) + x * C::kQBytes + (ch / 8) * C::kPanel;
             int loads = 0;
-            bool ok = true;
-            while (left > 0 && ok) {
-                const int n = seg_len();
-                const int rows = rows_of_item() - x * 128;
+            for (int k_seg = 0;; k_seg++) {
+                const Segment* g = open_segment(k_seg);
+                if (!g) break;
+                const int rows = g->rows - x * 128;
                 if (rows > 0) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[x], (loads & 1) ^ 1, lim) && !*abort_flag);
-                    if (!ok) break;
-                    const int ch = lane % L;
-                    for (int r = lane / L; r < 128; r += RW) {
-                        // rows behind the item's last repeat it: what they compute is not written
-                        const int rr = c.rb * R + x * 128 + min(r, rows - 1);
-                        const int i = div_group(p, rr), g = rr - i * p.group;
-                        cp_async_16(dst0 + (ch / 8) * C::kPanel + r * 128 + (((ch % 8) ^ (r & 7)) * 16),
-                                    p.q + (c.s.first + i) * p.q_token + (c.h * p.group + g) * p.q_head + ch * 8);
+                    const int r0 = g->rb * R + x * 128, h0 = g->h * p.group;
+                    const __nv_bfloat16* q0 = p.q + static_cast<int64_t>(g->first) * p.q_token;
+                    if (!(ok = wait(&q_empty[x], (loads & 1) ^ 1))) break;
+#pragma unroll 1
+                    for (int b = 0; b < 128; b += 32) {
+                        // where row b + lane lies; rows behind the item's last repeat it: what they compute is
+                        // not written
+                        const int rr = r0 + min(b + lane, rows - 1);
+                        const int i = div_group(p, rr);
+                        const int64_t at = i * p.q_token + (h0 + rr - i * p.group) * p.q_head;
+#pragma unroll
+                        for (int s = 0; s < 32; s += RW) {
+                            const int r = s + lane / L;
+                            const int64_t src = __shfl_sync(0xffffffffu, at, r);
+                            cp_async_16(dst0 + (b + r) * 128 + (((ch % 8) ^ (r & 7)) * 16), q0 + src + ch * 8);
+                        }
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     fence_proxy_async_smem();
                     mbar_arrive(&q_full[x]);
                     loads++;
                 }
-                seg_next(n);
+                close_segment(k_seg);
             }
             if (!ok && lane == 0) fail();
         }
     } else {
         regs_inc<kRegsSoftmax>();
         // ================================================================ softmax
-        const int x = wg - 1;            // slot
-        const int quarter = warp & 3;    // tensor-memory lanes this warp may access
+        const int x = wg - 1;             // slot
+        const int quarter = warp & 3;     // tensor-memory lanes this warp may access
         const int row = quarter * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32);
-        const uint32_t col_s = static_cast<uint32_t>(x * UK);
-        const uint32_t col_o = static_cast<uint32_t>(2 * UK + x * D);
+        const uint32_t t_s = tmem_addr(tmem, lane_base, static_cast<uint32_t>(x * UK));  // P is written over it
+        const uint32_t t_o = tmem_addr(tmem, lane_base, static_cast<uint32_t>(2 * UK + x * D));
         const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
         const int off = p.over_prefix ? 0 : p.prefix_len;
+        PassBounds bounds{0, 0};  // over the prefix: of all rows' positions
+        if (p.over_prefix) bounds = pass_bounds(p);
         int steps = 0, segs = 0;
         int pos = 0;  // ring items of the segments before
-        bool ok = true;
-        while (left > 0 && ok) {
-            const int n = seg_len();
-            const int rows = rows_of_item() - x * 128;  // of this slot
+        for (int k_seg = 0;; k_seg++) {
+            const Segment* g = open_segment(k_seg);
+            if (!g) break;
+            const int n = g->n;
+            const int rows = g->rows - x * 128;  // of this slot
             if (rows <= 0) {
                 pos += 2 * n;
-                seg_next(n);
+                close_segment(k_seg);
                 continue;
             }
-            const int r0 = c.rb * R + x * 128;
-            const int rr = r0 + min(row, rows - 1);
-            const int i_tok = div_group(p, rr);
-            const int base = p.prefix_len + c.s.p0;
-            // the slot's lowest and highest position, this row's, and the item's (whose keys are loaded)
-            const int p_lo = p.over_prefix ? piece.pb.lo : base + div_group(p, r0);
-            const int p_hi = p.over_prefix ? piece.pb.hi : base + div_group(p, r0 + min(rows, 128) - 1);
-            const int item_hi = p.over_prefix ? piece.pb.hi : base + div_group(p, c.rb * R + rows_of_item() - 1);
-            const bool look_up = p.over_prefix && !(p_lo >= p.prefix_len - 1 && p.window >= 0 && p_hi <= p.window);
-            const int pr = look_up ? token_position(p, c.s.first + i_tok) : p.over_prefix ? p_lo : base + i_tok;
-            const bool row_all = pr < p.n_global;
             float m_ref = -INFINITY;  // running max, log2 units of the scaled score
             float l_sum = 0.f;
+            int row_lo, row_hi, lo_lo, lo_hi, hi_lo, hi_item;  // keys seen: by this row, and over the slot's rows
+            {
+                const int r0 = g->rb * R + x * 128;
+                const int base = g->base;
+                const int i_tok = div_group(p, r0 + min(row, rows - 1));
+                const int p_lo = p.over_prefix ? bounds.lo : base + div_group(p, r0);
+                const int p_hi = p.over_prefix ? bounds.hi : base + div_group(p, r0 + min(rows, 128) - 1);
+                const int p_item = p.over_prefix ? bounds.hi : base + div_group(p, g->rb * R + g->rows - 1);
+                auto first_seen = [&](int q) {
+                    return q < p.n_global ? 0 : p.window >= 0 ? q - p.window - off : INT32_MAX;
+                };
+                const bool look_up = p.over_prefix && !(p_lo >= p.prefix_len - 1 && p.window >= 0 && p_hi <= p.window);
+                const int pr = look_up ? token_position(p, g->first + i_tok) : p.over_prefix ? p_lo : base + i_tok;
+                row_lo = first_seen(pr);
+                row_hi = min(pr - off, g->hi - 1);
+                lo_lo = first_seen(p_lo);
+                lo_hi = first_seen(p_hi);
+                hi_lo = min(p_lo - off, g->hi - 1);
+                hi_item = min(p_item - off, g->hi - 1);
+            }
+            const int cols = p.cols - off;
+#pragma unroll 1
             for (int j = 0; j < n; j++) {
-                const int kv0 = c.u.key(c.i + j, UK);
-                const int a = kv0 + off, z = a + UK - 1;  // positions of the tile's first and last key
-                const bool masked = !(kv0 + UK <= c.u.hi && z <= p_lo &&
-                                      ((p.window >= 0 && p_hi - a <= p.window) || z < p.cols || p_hi < p.n_global));
-                uint32_t allow[UK / 32];
-                if (masked) {
-                    const int dq = pr - a;
-                    const int c_max = min(dq, c.u.hi - 1 - kv0);
-#pragma unroll
-                    for (int w = 0; w < UK / 32; w++) {
-                        const int b = 32 * w;
-                        uint32_t m = bits_between(0, p.cols - 1 - a - b);
-                        if (p.window >= 0) m |= bits_between(dq - p.window - b, 31);
-                        if (row_all) m = 0xffffffffu;
-                        allow[w] = m & bits_between(0, c_max - b);
-                    }
-                    if (x == 0) {
-                        // this thread's V row of the tile, where no row of the item sees it
-                        const int kp = a + row;
-                        const bool seen = kv0 + row < c.u.hi && kp <= item_hi &&
-                                          (kp < p.cols || p_lo < p.n_global || (p.window >= 0 && p_lo - kp <= p.window));
-                        if (__any_sync(0xffffffffu, !seen)) {
-                            const int pv = pos + 2 * j + 1;
-                            ok = mbar_wait(&ring_full[pv % S], (pv / S) & 1, lim);
-                            ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-                            if (!ok) break;
-                            if (!seen) {
-                                uint8_t* v = ring + (pv % S) * C::kTileBytes + row * 128;
-#pragma unroll
-                                for (int pn = 0; pn < D / 64; pn++)
-#pragma unroll
-                                    for (int q = 0; q < 8; q++)
-                                        *reinterpret_cast<uint4*>(v + pn * C::kPanel + q * 16) = make_uint4(0u, 0u, 0u, 0u);
-                            }
-                            fence_proxy_async_smem();
+                const int kv0 = g->key(j);
+                const bool masked = !(kv0 + UK - 1 <= hi_lo && (kv0 >= lo_hi || kv0 + UK <= cols));
+                if (masked && x == 0) {
+                    // this thread's V row of the tile, where no row of the item sees it
+                    const int kp = kv0 + row;
+                    const bool seen = kp <= hi_item && (kp >= lo_lo || kp < cols);
+                    if (__any_sync(0xffffffffu, !seen)) {
+                        const int pv = pos + 2 * j + 1;
+                        if (!(ok = wait(&ring_full[pv % S], (pv / S) & 1))) break;
+                        if (!seen) {
+                            uint8_t* v = ring + (pv % S) * C::kTileBytes + row * 128;
+#pragma unroll 1
+                            for (int q = 0; q < D / 8; q++)
+                                *reinterpret_cast<uint4*>(v + (q / 8) * C::kPanel + (q % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
                         }
+                        fence_proxy_async_smem();
                     }
                 }
-
-                ok = mbar_wait(&s_full[x], steps & 1, lim);
-                ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-                if (!ok) break;
+                if (!(ok = wait(&s_full[x], steps & 1))) break;
                 tc_fence_after_sync();
-
                 float s[UK];
                 {
                     uint32_t r[UK / 32][32];
 #pragma unroll
-                    for (int q = 0; q < UK / 32; q++)
-                        tmem_ld_32x32b_x32(tmem_addr(tmem, lane_base, col_s + 32 * q), r[q]);
+                    for (int q = 0; q < UK / 32; q++) tmem_ld_32x32b_x32(t_s + 32 * q, r[q]);
                     tmem_wait_ld();
 #pragma unroll
                     for (int q = 0; q < UK / 32; q++) reg_fence(r[q]);
@@ -405,18 +449,22 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 if (masked) {
 #pragma unroll
-                    for (int q = 0; q < UK; q++) s[q] = (allow[q / 32] >> (q % 32)) & 1u ? s[q] : -INFINITY;
+                    for (int w = 0; w < UK / 32; w++) {
+                        const int b = kv0 + 32 * w;
+                        const uint32_t m = (bits_between(row_lo - b, 31) | bits_between(0, cols - 1 - b)) &
+                                           bits_between(0, row_hi - b);
+#pragma unroll
+                        for (int q = 0; q < 32; q++) s[32 * w + q] = (m >> q) & 1u ? s[32 * w + q] : -INFINITY;
+                    }
                 }
                 // row max: 16 independent chains of three-input max
                 float mx[16];
 #pragma unroll
-                for (int i = 0; i < 16; i++) mx[i] = fmax3(s[i], s[16 + i], s[32 + i]);
-#pragma unroll
-                for (int q = 48; q + 32 <= UK; q += 32)
-#pragma unroll
-                    for (int i = 0; i < 16; i++) mx[i] = fmax3(mx[i], s[q + i], s[q + 16 + i]);
-#pragma unroll
-                for (int i = 0; i < 16; i++) mx[i] = fmaxf(mx[i], s[UK - 16 + i]);
+                for (int i = 0; i < 16; i++) {
+                    mx[i] = fmax3(s[i], s[16 + i], s[32 + i]);
+                    mx[i] = fmax3(mx[i], s[48 + i], s[64 + i]);
+                    mx[i] = fmaxf(fmax3(mx[i], s[80 + i], s[96 + i]), s[112 + i]);
+                }
                 const float m_tile =
                     fmax3(fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmax3(mx[6], mx[7], mx[8])),
                           fmax3(fmax3(mx[9], mx[10], mx[11]), fmax3(mx[12], mx[13], mx[14]), mx[15]), -INFINITY) *
@@ -440,7 +488,7 @@ __global__ void __launch_bounds__(384, 1)
                     for (int i = 0; i < 32; i++) {
                         const uint64_t x2 = f2_fma(f2_pack(s[q + 2 * i], s[q + 2 * i + 1]), scale2, neg_m);
                         float e0, e1;
-                        if (((q / 2 + i) & 7) < 2) {
+                        if ((i & 7) < 2) {
                             exp2_poly_x2(x2, e0, e1);
                         } else {
                             float x0, x1;
@@ -451,93 +499,91 @@ __global__ void __launch_bounds__(384, 1)
                         acc[i & 3] = f2_add(acc[i & 3], f2_pack(e0, e1));
                         pk[i] = pack_bf16x2(e0, e1);
                     }
-                    tmem_st_32x32b_x32(tmem_addr(tmem, lane_base, col_s + q / 2), pk);
+                    tmem_st_32x32b_x32(t_s + q / 2, pk);
                 }
                 {
-                    float a0, a1, b0, b1, c0, c1, d0, d1;
-                    f2_unpack(acc[0], a0, a1);
-                    f2_unpack(acc[1], b0, b1);
-                    f2_unpack(acc[2], c0, c1);
-                    f2_unpack(acc[3], d0, d1);
-                    l_sum += ((a0 + a1) + (b0 + b1)) + ((c0 + c1) + (d0 + d1));
+                    float a0, a1, b0, b1;
+                    f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
+                    f2_unpack(f2_add(acc[2], acc[3]), b0, b1);
+                    l_sum += (a0 + a1) + (b0 + b1);
                 }
                 if (j > 0 && __any_sync(0xffffffffu, grow)) {
                     // O_X holds every product up to tile j-1 (the commit of S_X(j) covers PV_X(j-1))
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < D; q += 32) {
                         uint32_t r[32];
-                        tmem_ld_32x32b_x32(tmem_addr(tmem, lane_base, col_o + q), r);
+                        tmem_ld_32x32b_x32(t_o + q, r);
                         tmem_wait_ld();
                         reg_fence(r);
 #pragma unroll
                         for (int i = 0; i < 32; i++) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-                        tmem_st_32x32b_x32(tmem_addr(tmem, lane_base, col_o + q), r);
+                        tmem_st_32x32b_x32(t_o + q, r);
                     }
                 }
                 tmem_wait_st();
                 tc_fence_before_sync();
-                mbar_arrive(&p_full[x]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
                 steps++;
             }
             if (!ok) break;
             // ---------------------------------------------------------------- end of the segment
-            ok = mbar_wait(&o_full[x], segs & 1, lim);
-            ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-            if (!ok) break;
-            uint32_t o[D / 32][32];
+            if (!(ok = wait(&o_full[x], segs & 1))) break;
             tc_fence_after_sync();
-#pragma unroll
-            for (int q = 0; q < D / 32; q++) tmem_ld_32x32b_x32(tmem_addr(tmem, lane_base, col_o + 32 * q), o[q]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int q = 0; q < D / 32; q++) reg_fence(o[q]);
-            tc_fence_before_sync();
-            mbar_arrive(&o_empty[x]);
-            segs++;
-            if (row < rows) {
-                const int u_item = piece.u0 + (total - left) - c.i;
-                const bool begins = u_item >= piece.u0, whole = begins && u_item + c.u.nt <= piece.u1;
-                const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0)) * R + x * 128 + row;
-                const int64_t t = c.s.first + i_tok;
-                const int hq = c.h * p.group + rr - i_tok * p.group;
-                const int64_t at = t * p.Hq + hq;
-                if (begins) {
-                    RowInfo ri{0, 0, 0, 0};
-                    if (!whole) {
-                        const int n_parts = cta_of(piece, u_item + c.u.nt - 1) - static_cast<int>(blockIdx.x) + 1;
-                        ri = RowInfo{p.part_row0 + static_cast<int32_t>(slot), p.part_row0 + static_cast<int32_t>(slot) + R,
-                                     n_parts, 2 * R};
-                    }
-                    p.info[at] = ri;
-                }
+            const int r0 = g->rb * R + x * 128;
+            const int rr = r0 + min(row, rows - 1);
+            const int i_tok = div_group(p, rr);
+            const int64_t t = g->first + i_tok;
+            const int hq = g->h * p.group + rr - i_tok * p.group;
+            const int64_t at = t * p.Hq + hq;
+            const bool begins = g->begins, whole = g->whole;
+            const int slot = (2 * static_cast<int>(blockIdx.x) + (begins ? 1 : 0)) * R + x * 128 + row;
+            const int parts = g->parts;
+            const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
+            const bool write = row < rows;
+#pragma unroll 1
+            for (int q = 0; q < D; q += 32) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(t_o + q, o);
+                tmem_wait_ld();
+                reg_fence(o);
+                if (!write) continue;
                 if (whole && p.acc == nullptr) {
-                    const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
-                    uint4* dst = reinterpret_cast<uint4*>(p.o + t * p.o_token + hq * p.o_head);
+                    uint4* dst = reinterpret_cast<uint4*>(p.o + t * p.o_token + hq * p.o_head + q);
 #pragma unroll
-                    for (int q = 0; q < D; q += 8) {
-                        const uint32_t* oc = &o[q / 32][q % 32];
+                    for (int i = 0; i < 32; i += 8) {
                         uint4 v;
-                        v.x = pack_bf16x2(__uint_as_float(oc[0]) * inv, __uint_as_float(oc[1]) * inv);
-                        v.y = pack_bf16x2(__uint_as_float(oc[2]) * inv, __uint_as_float(oc[3]) * inv);
-                        v.z = pack_bf16x2(__uint_as_float(oc[4]) * inv, __uint_as_float(oc[5]) * inv);
-                        v.w = pack_bf16x2(__uint_as_float(oc[6]) * inv, __uint_as_float(oc[7]) * inv);
-                        dst[q / 8] = v;
+                        v.x = pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+                        v.y = pack_bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+                        v.z = pack_bf16x2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
+                        v.w = pack_bf16x2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+                        dst[i / 8] = v;
                     }
-                    p.lse[at] = l_sum > 0.f ? (m_ref + log2f(l_sum)) * 0.69314718055994530942f : -INFINITY;
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(whole ? p.acc + at * D : p.part_o + slot * D);
+                    uint4* dst = reinterpret_cast<uint4*>((whole ? p.acc + at * D : p.part_o + static_cast<int64_t>(slot) * D) + q);
 #pragma unroll
-                    for (int q = 0; q < D; q += 4) {
-                        const uint32_t* oc = &o[q / 32][q % 32];
-                        dst[q / 4] = make_uint4(oc[0], oc[1], oc[2], oc[3]);
-                    }
-                    (whole ? p.acc_ml[at] : p.part_ml[slot]) = make_float2(m_ref, l_sum);
+                    for (int i = 0; i < 32; i += 4) dst[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 }
             }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_empty[x]);  // O_X may now be overwritten
+            segs++;
+            if (write) {
+                if (whole && p.acc == nullptr)
+                    p.lse[at] = l_sum > 0.f ? (m_ref + log2f(l_sum)) * 0.69314718055994530942f : -INFINITY;
+                else
+                    (whole ? p.acc_ml[at] : p.part_ml[slot]) = make_float2(m_ref, l_sum);
+                if (begins && p.info != nullptr)
+                    p.info[at] = whole ? RowInfo{0, 0, 0, 0}
+                                       : RowInfo{p.part_row0 + slot, p.part_row0 + slot + R, parts, 2 * R};
+                if (begins && !whole && p.tails != nullptr)
+                    p.tails[blockIdx.x * R + x * 128 + row] = TailRow{static_cast<int32_t>(at), parts};
+            }
             pos += 2 * n;
-            seg_next(n);
+            close_segment(k_seg);
         }
-        if (!ok) fail();
+        if (!ok && lane == 0) fail();
     }
 
     tc_fence_before_sync();

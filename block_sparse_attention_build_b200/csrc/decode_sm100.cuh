@@ -139,6 +139,8 @@ __global__ void __launch_bounds__(128, 2)
         fence_barrier_init();
     }
     __syncwarp();
+    // no tail rows yet (a segment's end, where there may be some, lies behind barriers)
+    if (!ITEMS && p.tails != nullptr && tid < R) p.tails[blockIdx.x * R + tid] = TailRow{0, 0};
     const int rank = ITEMS ? static_cast<int>(cluster_rank()) : 0;
     const int CL = ITEMS ? static_cast<int>(cluster_size()) : 1;
     const Piece piece = ITEMS ? find_piece<R, UK, true>(p, ahead, blockIdx.x / CL, gridDim.x / CL)
@@ -504,6 +506,8 @@ __global__ void __launch_bounds__(128, 2)
                 for (int i = 0; i < N; i++) *reinterpret_cast<float2*>(dst + i * 8) = make_float2(v[i][0], v[i][1]);
                 if (first) (whole ? p.acc_ml[at] : p.part_ml[slot + r]) = make_float2(m, l);
             }
+            if (!ITEMS && first && p.tails != nullptr && begins && !whole)
+                p.tails[blockIdx.x * R + r] = TailRow{static_cast<int32_t>(at), ri.n};
             if (first && p.info != nullptr && begins)
                 p.info[at] = RowInfo{ri.first + (whole ? 0 : r), ri.second + (whole ? 0 : r), ri.n, ri.stride};
         };

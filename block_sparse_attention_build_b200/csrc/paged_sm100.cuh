@@ -42,6 +42,12 @@ struct alignas(16) RowInfo {
     int32_t first, second, n, stride;
 };
 
+// The same from the other side, where rows are many and few of them are cut: the
+// rows of each CTA's tail slot (n = 0: none), R entries a CTA.
+struct alignas(8) TailRow {
+    int32_t row, n;  // token * Hq + head; parts
+};
+
 struct PassParams {
     const __nv_bfloat16* q;
     int64_t q_token, q_head;
@@ -64,7 +70,8 @@ struct PassParams {
     float* part_o;             // [2 * CTAs * R, D] parts of cut items (this pass's)
     float2* part_ml;           // [2 * CTAs * R] running maximum (log2 units), sum
     int32_t part_row0;         // index of the first of them in the arrays that join_kernel reads
-    RowInfo* info;             // [T, Hq]; null where no row is read from parts
+    RowInfo* info;             // [T, Hq]; null where no row is read from parts or where there are
+    TailRow* tails;            // [CTAs * R]
     float* acc;                // null: finished rows go to o and lse; else [T, Hq, D] unnormalised,
     float2* acc_ml;            // [T, Hq]
     const float* pre_acc;      // not null: what the pass over the prefix left, added to every row
@@ -230,6 +237,21 @@ __device__ __forceinline__ int seq_units(const PassParams& p, const PassBounds& 
     return n * p.Hkv;
 }
 
+// Over the prefix: the lowest and the highest position of all sequences' rows (whole warp).
+__device__ __forceinline__ PassBounds pass_bounds(const PassParams& p)
+{
+    int lo = INT32_MAX, hi = INT32_MIN;
+#pragma unroll 1
+    for (int b = threadIdx.x % 32; b < p.B; b += 32) {
+        const int m = __ldg(&p.q_start[b + 1]) - __ldg(&p.q_start[b]);
+        const int last = p.prefix_len + cached_len(p, b) - 1;
+        if (m <= 0) continue;
+        lo = min(lo, last - m + 1);
+        hi = max(hi, last);
+    }
+    return PassBounds{__reduce_min_sync(0xffffffffu, lo), __reduce_max_sync(0xffffffffu, hi)};
+}
+
 // The sequence that find_piece looks at first in this lane.
 __device__ __forceinline__ SeqView peek_seq(const PassParams& p)
 {
@@ -248,19 +270,7 @@ __device__ __forceinline__ Piece find_piece(const PassParams& p, const SeqView& 
     Piece r;
     r.pb = PassBounds{0, 0};
     const int n_seq = p.over_prefix ? 1 : p.B;
-    if (p.over_prefix) {
-        // the rows' positions: the lowest and the highest of all sequences
-        int lo = INT32_MAX, hi = INT32_MIN;
-#pragma unroll 1
-        for (int b = lane; b < p.B; b += 32) {
-            const int m = __ldg(&p.q_start[b + 1]) - __ldg(&p.q_start[b]);
-            const int last = p.prefix_len + cached_len(p, b) - 1;
-            if (m <= 0) continue;
-            lo = min(lo, last - m + 1);
-            hi = max(hi, last);
-        }
-        r.pb = PassBounds{__reduce_min_sync(kAll, lo), __reduce_max_sync(kAll, hi)};
-    }
+    if (p.over_prefix) r.pb = pass_bounds(p);
     // units of this lane's sequences, and of those before them
     const int per = (n_seq + 31) / 32;
     const int b0 = lane * per, b1 = min(b0 + per, n_seq);
@@ -363,12 +373,87 @@ struct JoinParams {
     int32_t part_rows;        // rows of the part arrays
 };
 
-// Rows whose result lies in parts (and, with a prefix, all rows): O = sum of
-// O_k 2^(m_k - M) over sum of l_k 2^(m_k - M), M the largest m_k, in the order of
-// the parts.  WPR warps share a row (each takes every WPR-th part, then they are
-// added in the order of the warps): one where rows are many, eight where a few
-// rows have up to a part per CTA, whose loads are then in flight together.
-template <int D, int WPR, int kGroup, bool PREFIX>
+// Up to two kernels' tail rows: entry e of a kernel is row e mod R of CTA e / R.
+struct TailJoinParams {
+    const float* part_o;
+    const float2* part_ml;
+    const TailRow* tails[2];
+    int32_t entries[2], shift[2];  // entries (0: none), log2 R
+    int32_t part_row0[2];
+    __nv_bfloat16* o;
+    int64_t o_token, o_head;
+    float* lse;
+    int32_t Hq, rows;              // T * Hq
+    int32_t part_rows;
+};
+
+// A row's parts added up by one warp, E elements a lane: O = sum of O_k 2^(m_k - M)
+// over L = sum of l_k 2^(m_k - M), M the largest m_k, in the order they come.
+template <int D>
+struct RowSum {
+    static constexpr int E = D / 32;
+    float acc[E];
+    float M, L;
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int e = 0; e < E; e++) acc[e] = 0.f;
+        M = -INFINITY;
+        L = 0.f;
+    }
+    __device__ __forceinline__ void add(const float (&v)[E], float2 ml)
+    {
+        if (ml.x == -INFINITY) return;
+        const float mn = fmaxf(M, ml.x);
+        const float a = ex2_approx(M - mn), b = ex2_approx(ml.x - mn);
+#pragma unroll
+        for (int e = 0; e < E; e++) acc[e] = acc[e] * a + v[e] * b;
+        L = L * a + ml.y * b;
+        M = mn;
+    }
+    // parts first, second, second + stride, ...: every `step`-th from k0 on, four in flight
+    __device__ __forceinline__ void add_parts(const float* part_o, const float2* part_ml, const RowInfo& ri, int k0,
+                                              int step, int lane)
+    {
+        constexpr int K = 4;
+        for (int k1 = k0; k1 < ri.n; k1 += K * step) {
+            float v[K][E];
+            float2 ml[K];
+#pragma unroll
+            for (int j = 0; j < K; j++) {
+                const int k = k1 + j * step;
+                ml[j] = make_float2(-INFINITY, 0.f);
+                if (k >= ri.n) continue;
+                const int64_t at = k == 0 ? ri.first : ri.second + static_cast<int64_t>(k - 1) * ri.stride;
+                ml[j] = part_ml[at];
+#pragma unroll
+                for (int e = 0; e < E; e++) v[j][e] = part_o[at * D + lane * E + e];
+            }
+#pragma unroll
+            for (int j = 0; j < K; j++) add(v[j], ml[j]);
+        }
+    }
+    template <class P>
+    __device__ __forceinline__ void write(const P& p, uint32_t row, int lane) const
+    {
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const uint32_t t = row / static_cast<uint32_t>(p.Hq), h = row - t * p.Hq;
+        __nv_bfloat16* dst = p.o + t * p.o_token + h * p.o_head + lane * E;
+        if constexpr (E == 4)
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+        if (lane == 0) p.lse[row] = L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+    }
+};
+
+
+// Rows whose result lies in parts (and, with a prefix, all rows).  WPR warps share
+// a row (each takes every WPR-th part, then they are added in the order of the
+// warps): one where rows are many, eight where a few rows have up to a part per CTA,
+// whose loads are then in flight together.
+template <int D, int WPR, bool PREFIX>
 __global__ void __launch_bounds__(256) join_kernel(const JoinParams p)
 {
     constexpr int kRows = 8 / WPR;
@@ -379,112 +464,117 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p)
     __shared__ float sh_o[8][D];
     __shared__ float sh_m[8], sh_l[8];
     const int64_t total = static_cast<int64_t>(min(max(__ldg(&p.q_start[p.B]), 0), p.T)) * p.Hq;
-    // A warp looks at kGroup rows at once (most rows may be finished already) and takes them one by one; where
-    // warps share a row, every warp of a block makes the same number of rounds.
-    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows * kGroup; row0 < total;
-         row0 += static_cast<int64_t>(gridDim.x) * kRows * kGroup) {
-        const int64_t base = row0 + warp / WPR * kGroup;
-        RowInfo ris[2] = {{-1, 0, 0, 0}, {-1, 0, 0, 0}};
-        bool todo = false;
-        if (lane < kGroup && base + lane < total) {
+    // every warp of a block makes the same number of rounds
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < total;
+         row0 += static_cast<int64_t>(gridDim.x) * kRows) {
+        const int64_t row = row0 + warp / WPR;
+        bool write = PREFIX && row < total;
+        RowSum<D> sum;
+        sum.clear();
+        if (row < total) {
 #pragma unroll
             for (int s = 0; s < (PREFIX ? 2 : 1); s++) {
-                RowInfo ri = p.info[s][base + lane];
+                const RowInfo ri = p.info[s][row];
                 // a row that no sequence covers (q_start not ascending from 0) has no entry: nothing of it
                 // is followed
                 if (ri.n < 0 || ri.n > p.part_rows || ri.stride < 0 || ri.stride > p.part_rows || ri.first < 0 ||
                     ri.second < 0 ||
                     (ri.n > 0 && (ri.first >= p.part_rows ||
                                   ri.second + static_cast<int64_t>(ri.n - 2) * ri.stride >= p.part_rows)))
-                    ri.n = -1;
-                ris[s] = ri;
-                todo = todo || PREFIX || ri.n > 0;
-            }
-        }
-        for (uint32_t mask = __ballot_sync(0xffffffffu, todo), r = 0; WPR > 1 ? r == 0 : mask != 0; r++) {
-            const int src = WPR > 1 ? 0 : __ffs(mask) - 1;
-            const bool write = WPR > 1 ? mask != 0 : true;
-            mask &= mask - 1;
-            const int64_t row = base + src;
-            float acc[E];
-#pragma unroll
-            for (int e = 0; e < E; e++) acc[e] = 0.f;
-            float M = -INFINITY, L = 0.f;
-            auto add = [&](const float* v, float2 ml) {
-                if (ml.x == -INFINITY) return;
-                const float mn = fmaxf(M, ml.x);
-                const float a = ex2_approx(M - mn), b = ex2_approx(ml.x - mn);
-#pragma unroll
-                for (int e = 0; e < E; e++) acc[e] = acc[e] * a + v[e] * b;
-                L = L * a + ml.y * b;
-                M = mn;
-            };
-#pragma unroll
-            for (int s = 0; s < (PREFIX ? 2 : 1); s++) {
-                RowInfo ri;
-                ri.first = __shfl_sync(0xffffffffu, ris[s].first, src);
-                ri.second = __shfl_sync(0xffffffffu, ris[s].second, src);
-                ri.n = __shfl_sync(0xffffffffu, ris[s].n, src);
-                ri.stride = __shfl_sync(0xffffffffu, ris[s].stride, src);
-                if (!write) continue;
+                    continue;
                 if (ri.n == 0) {
                     if (PREFIX && sub == 0) {
                         float v[E];
 #pragma unroll
                         for (int e = 0; e < E; e++) v[e] = p.acc[s][row * D + lane * E + e];
-                        add(v, p.acc_ml[s][row]);
+                        sum.add(v, p.acc_ml[s][row]);
                     }
                     continue;
                 }
-                constexpr int K = 4;  // parts in flight
-                for (int k0 = sub; k0 < ri.n; k0 += K * WPR) {
-                    float v[K][E];
-                    float2 ml[K];
-#pragma unroll
-                    for (int j = 0; j < K; j++) {
-                        const int k = k0 + j * WPR;
-                        ml[j] = make_float2(-INFINITY, 0.f);
-                        if (k >= ri.n) continue;
-                        const int64_t at = k == 0 ? ri.first : ri.second + static_cast<int64_t>(k - 1) * ri.stride;
-                        ml[j] = p.part_ml[at];
-#pragma unroll
-                        for (int e = 0; e < E; e++) v[j][e] = p.part_o[at * D + lane * E + e];
-                    }
-#pragma unroll
-                    for (int j = 0; j < K; j++) add(v[j], ml[j]);
-                }
-            }
-            if constexpr (WPR > 1) {
-#pragma unroll
-                for (int e = 0; e < E; e++) sh_o[warp][lane * E + e] = acc[e];
-                if (lane == 0) {
-                    sh_m[warp] = M;
-                    sh_l[warp] = L;
-                }
-                __syncthreads();
-                if (sub == 0) {
-                    for (int w = 1; w < WPR; w++) {
-                        float v[E];
-#pragma unroll
-                        for (int e = 0; e < E; e++) v[e] = sh_o[warp + w][lane * E + e];
-                        add(v, make_float2(sh_m[warp + w], sh_l[warp + w]));
-                    }
-                }
-                __syncthreads();
-            }
-            if (write && sub == 0) {
-                const float inv = L > 0.f ? 1.f / L : 0.f;
-                const uint32_t t = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.Hq), h = static_cast<uint32_t>(row) - t * p.Hq;
-                __nv_bfloat16* dst = p.o + t * p.o_token + h * p.o_head + lane * E;
-                if constexpr (E == 4)
-                    *reinterpret_cast<uint2*>(dst) =
-                        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-                else
-                    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-                if (lane == 0) p.lse[row] = L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+                write = true;
+                sum.add_parts(p.part_o, p.part_ml, ri, sub, WPR, lane);
             }
         }
+        if constexpr (WPR > 1) {
+#pragma unroll
+            for (int e = 0; e < E; e++) sh_o[warp][lane * E + e] = sum.acc[e];
+            if (lane == 0) {
+                sh_m[warp] = sum.M;
+                sh_l[warp] = sum.L;
+            }
+            __syncthreads();
+            if (sub == 0) {
+                for (int w = 1; w < WPR; w++) {
+                    float v[E];
+#pragma unroll
+                    for (int e = 0; e < E; e++) v[e] = sh_o[warp + w][lane * E + e];
+                    sum.add(v, make_float2(sh_m[warp + w], sh_l[warp + w]));
+                }
+            }
+            __syncthreads();
+        }
+        if (write && sub == 0) sum.write(p, static_cast<uint32_t>(row), lane);
     }
+}
+
+// The rows of the CTAs' tail slots, eight lanes each: most have two parts, so what
+// counts is how many rows' loads a warp has in flight.
+template <int D>
+__global__ void __launch_bounds__(256) join_tails_kernel(const TailJoinParams p)
+{
+    constexpr int E = D / 8, V = E / 4;  // elements and 16-byte loads of a lane (those of a load lie side by side)
+    wait_previous_kernel();
+    const int l = threadIdx.x % 8;
+    int e = (blockIdx.x * 256 + threadIdx.x) / 8;
+    const int k = e >= p.entries[0];
+    if (k) e -= p.entries[0];
+    if (e >= p.entries[k]) return;
+    const TailRow t = p.tails[k][e];
+    const int R = 1 << p.shift[k];
+    const int64_t first = p.part_row0[k] + (2 * (e >> p.shift[k]) + 1) * R + (e & (R - 1));
+    // part i at rows first, first + R, first + 3 R, ...
+    if (t.n <= 0 || t.row < 0 || t.row >= p.rows || first + (2 * static_cast<int64_t>(t.n) - 3) * R >= p.part_rows) return;
+    float acc[E];
+#pragma unroll
+    for (int i = 0; i < E; i++) acc[i] = 0.f;
+    float M = -INFINITY, L = 0.f;
+    for (int i0 = 0; i0 < t.n; i0 += 2) {
+        float4 v[2][V];
+        float2 ml[2];
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const int i = i0 + j;
+            ml[j] = make_float2(-INFINITY, 0.f);
+            if (i >= t.n) continue;
+            const int64_t at = i == 0 ? first : first + (2 * i - 1) * R;
+            ml[j] = p.part_ml[at];
+#pragma unroll
+            for (int x = 0; x < V; x++) v[j][x] = *reinterpret_cast<const float4*>(p.part_o + at * D + (x * 8 + l) * 4);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            if (ml[j].x == -INFINITY) continue;
+            const float mn = fmaxf(M, ml[j].x);
+            const float a = ex2_approx(M - mn), b = ex2_approx(ml[j].x - mn);
+#pragma unroll
+            for (int x = 0; x < V; x++) {
+                acc[4 * x] = acc[4 * x] * a + v[j][x].x * b;
+                acc[4 * x + 1] = acc[4 * x + 1] * a + v[j][x].y * b;
+                acc[4 * x + 2] = acc[4 * x + 2] * a + v[j][x].z * b;
+                acc[4 * x + 3] = acc[4 * x + 3] * a + v[j][x].w * b;
+            }
+            L = L * a + ml[j].y * b;
+            M = mn;
+        }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const uint32_t tok = static_cast<uint32_t>(t.row) / static_cast<uint32_t>(p.Hq), h = t.row - tok * p.Hq;
+    __nv_bfloat16* dst = p.o + tok * p.o_token + h * p.o_head + l * 4;
+#pragma unroll
+    for (int x = 0; x < V; x++)
+        *reinterpret_cast<uint2*>(dst + x * 32) = make_uint2(pack_bf16x2(acc[4 * x] * inv, acc[4 * x + 1] * inv),
+                                                             pack_bf16x2(acc[4 * x + 2] * inv, acc[4 * x + 3] * inv));
+    if (l == 0) p.lse[t.row] = L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
 }
 
 }  // namespace sa
