@@ -60,7 +60,9 @@ struct ChunkCfg {
     static constexpr int kPanel = 128 * 128;                 // 64 columns x 128 rows
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kOffRing = 2 * kQBytes;
-    static constexpr int kOffSeg = kOffRing + kStages * kTileBytes;
+    static constexpr int kStageRow = 80;  // 64 bytes of a row: 16-byte accesses of consecutive rows meet no bank twice
+    static constexpr int kOffStage = kOffRing + kStages * kTileBytes;  // a softmax warp's 32 rows each
+    static constexpr int kOffSeg = kOffStage + 8 * 32 * kStageRow;
     static constexpr int kOffBar = kOffSeg + 2 * static_cast<int>(sizeof(Segment));
     static constexpr int kNumBars = 2 * kStages + 2 * 6 + 2 * 2 + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
@@ -75,6 +77,31 @@ struct ChunkCfg {
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// 2^x for two lanes on the FMA pipe, as exp2_poly_x2 but of degree 5 (relative error
+// 2.2e-7, fitted by csrc/fit_exp2.py): the sum, which the LSE is taken from, then keeps
+// 32 bits' worth.  With degree 3 the LSE of rows with few keys was off by 7e-5; the two
+// terms more cost half a percent.
+__device__ __forceinline__ void exp2_poly5_x2(uint64_t x2, float& p0, float& p1)
+{
+    constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: x + kRound rounds x to an integer
+    const uint64_t t2 = f2_add(x2, f2_pack(kRound, kRound));
+    const uint64_t j2 = f2_add(t2, f2_pack(-kRound, -kRound));
+    const uint64_t f2 = f2_fma(j2, f2_pack(-1.f, -1.f), x2);
+    uint64_t q2 = f2_fma(f2_pack(0.0013276472454890609f, 0.0013276472454890609f), f2,
+                         f2_pack(0.009675540961325169f, 0.009675540961325169f));
+    q2 = f2_fma(q2, f2, f2_pack(0.05550713092088699f, 0.05550713092088699f));
+    q2 = f2_fma(q2, f2, f2_pack(0.24022120237350464f, 0.24022120237350464f));
+    q2 = f2_fma(q2, f2, f2_pack(0.6931469440460205f, 0.6931469440460205f));
+    q2 = f2_fma(q2, f2, f2_pack(1.0000001192092896f, 1.0000001192092896f));
+    float x0, x1, t0, t1, q0, q1;
+    f2_unpack(x2, x0, x1);
+    f2_unpack(t2, t0, t1);
+    f2_unpack(q2, q0, q1);
+    // the low bits of t hold j (two's complement); shifting them into the exponent field scales by 2^j
+    p0 = x0 < -125.f ? 0.f : __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
+    p1 = x1 < -125.f ? 0.f : __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
 }
 
 template <int D>
@@ -106,7 +133,7 @@ __global__ void __launch_bounds__(384, 1)
 
     launch_dependents();
     if (p.tails != nullptr && threadIdx.x < R) p.tails[blockIdx.x * R + threadIdx.x] = TailRow{0, 0};
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 64) {
         for (int i = 0; i < S; i++) {
             mbar_init(&ring_full[i], 1);
             mbar_init(&ring_empty[i], 1);
@@ -129,6 +156,8 @@ __global__ void __launch_bounds__(384, 1)
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
     }
+    Piece piece;
+    if (warp == 0) piece = find_piece<R, UK, false>(p, peek_seq(p), blockIdx.x, gridDim.x);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -160,7 +189,6 @@ __global__ void __launch_bounds__(384, 1)
         regs_dec<kRegsControl>();
         if (warp == 0) {
             // ============================================================ producer
-            const Piece piece = find_piece<R, UK, false>(p, peek_seq(p), blockIdx.x, gridDim.x);
             const int n_seq = p.over_prefix ? 1 : p.B;
             const int page_rows = min(1 << p.page_shift, UK);
             constexpr int P = D / 64;  // column panels
@@ -375,6 +403,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32);
         const uint32_t t_s = tmem_addr(tmem, lane_base, static_cast<uint32_t>(x * UK));  // P is written over it
         const uint32_t t_o = tmem_addr(tmem, lane_base, static_cast<uint32_t>(2 * UK + x * D));
+        uint8_t* stage = smem + C::kOffStage + (warp - 4) * 32 * C::kStageRow;
         const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
         const int off = p.over_prefix ? 0 : p.prefix_len;
         PassBounds bounds{0, 0};  // over the prefix: of all rows' positions
@@ -479,7 +508,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
                 const uint64_t neg_m = f2_pack(-m_use, -m_use);
-                // p = 2^(s * scale_log2 - m): 6 of every 8 pairs on the MUFU unit, 2 on the FMA pipe
+                // p = 2^(s * scale_log2 - m): 7 of every 8 pairs on the MUFU unit, 1 on the FMA pipe (2: 1 % slower)
                 uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int q = 0; q < UK; q += 64) {
@@ -488,8 +517,8 @@ __global__ void __launch_bounds__(384, 1)
                     for (int i = 0; i < 32; i++) {
                         const uint64_t x2 = f2_fma(f2_pack(s[q + 2 * i], s[q + 2 * i + 1]), scale2, neg_m);
                         float e0, e1;
-                        if ((i & 7) < 2) {
-                            exp2_poly_x2(x2, e0, e1);
+                        if ((i & 7) < 1) {
+                            exp2_poly5_x2(x2, e0, e1);
                         } else {
                             float x0, x1;
                             f2_unpack(x2, x0, x1);
@@ -541,28 +570,52 @@ __global__ void __launch_bounds__(384, 1)
             const int parts = g->parts;
             const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
             const bool write = row < rows;
+            const bool final = whole && p.acc == nullptr;
+            // Rows leave through a small buffer of the warp, 64 bytes of each at a time, so that a store writes
+            // whole sectors of eight rows (a thread per row writes 32 half sectors: 7900 cycles for 256 rows).
+            uint8_t* own = nullptr;
+            if (write)
+                own = final   ? reinterpret_cast<uint8_t*>(p.o + t * p.o_token + hq * p.o_head)
+                      : whole ? reinterpret_cast<uint8_t*>(p.acc + at * D)
+                              : reinterpret_cast<uint8_t*>(p.part_o + static_cast<int64_t>(slot) * D);
+            uint8_t* dst[4];  // this lane's 16 bytes of rows lane / 4 + 8 i
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint64_t d = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(own), lane / 4 + 8 * i);
+                dst[i] = d ? reinterpret_cast<uint8_t*>(d) + lane % 4 * 16 : nullptr;
+            }
+            auto pass_on = [&](int offset) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(stage + (lane / 4 + 8 * i) * C::kStageRow + lane % 4 * 16);
+                    if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + offset) = v;
+                }
+                __syncwarp();
+            };
+            uint4* in = reinterpret_cast<uint4*>(stage + lane * C::kStageRow);
 #pragma unroll 1
             for (int q = 0; q < D; q += 32) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(t_o + q, o);
                 tmem_wait_ld();
                 reg_fence(o);
-                if (!write) continue;
-                if (whole && p.acc == nullptr) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.o + t * p.o_token + hq * p.o_head + q);
+                if (final) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint4 v;
-                        v.x = pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-                        v.y = pack_bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-                        v.z = pack_bf16x2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
-                        v.w = pack_bf16x2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
-                        dst[i / 8] = v;
-                    }
+                    for (int i = 0; i < 32; i += 8)
+                        in[i / 8] = make_uint4(pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv),
+                                               pack_bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv),
+                                               pack_bf16x2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv),
+                                               pack_bf16x2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv));
+                    pass_on(q * 2);
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>((whole ? p.acc + at * D : p.part_o + static_cast<int64_t>(slot) * D) + q);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) dst[i / 4] = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int h = 0; h < 32; h += 16) {
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            in[i] = make_uint4(o[h + 4 * i], o[h + 4 * i + 1], o[h + 4 * i + 2], o[h + 4 * i + 3]);
+                        pass_on((q + h) * 4);
+                    }
                 }
             }
             tc_fence_before_sync();
