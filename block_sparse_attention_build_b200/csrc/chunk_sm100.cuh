@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(384, 1)
         if (warp == 0) {
             // ============================================================ producer
             const int n_seq = p.over_prefix ? 1 : p.B;
-            const int page_rows = min(1 << p.page_shift, UK);
+            const int row_shift = min(p.page_shift, 7), page_rows = 1 << row_shift;  // rows of one box
             constexpr int P = D / 64;  // column panels
             const int box = lane / P, panel = lane % P;
             Cursor c = piece.c;
@@ -226,12 +226,12 @@ __global__ void __launch_bounds__(384, 1)
                 // the pages of a tile are looked up while the one before it is loaded
                 auto tile_key = [&](int j) { return c.u.key(c.i + j, UK); };
                 auto boxes = [&](int k0) {
-                    return min(max((c.u.hi - k0 + page_rows - 1) / page_rows, 0), UK / page_rows);
+                    return min(max((c.u.hi - k0 + page_rows - 1) >> row_shift, 0), UK >> row_shift);
                 };
-                auto page_at = [&](int k0) { return box < boxes(k0) ? page_of(p, c.b, k0 + box * page_rows) : 0; };
+                auto page_at = [&](int k0) { return box < boxes(k0) ? page_entry(p, c.b, k0 + box * page_rows) : 0; };
                 int pg_next = page_at(tile_key(0));
                 for (int j = 0; j < n && ok; j++) {
-                    const int k0 = tile_key(j), nb = boxes(k0), pg = pg_next;
+                    const int k0 = tile_key(j), nb = boxes(k0), pg = page_of(p, pg_next);
                     if (j + 1 < n) pg_next = page_at(tile_key(j + 1));
                     const int row = (k0 + box * page_rows) & ((1 << p.page_shift) - 1);
 #pragma unroll 1

@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(128, 2)
     const int n_seq = p.over_prefix ? 1 : p.B;
 
     // ---- loads: this warp's tile of every unit of the piece, ST tiles ahead
-    const int page_rows = min(1 << p.page_shift, TK);  // rows of one box
+    constexpr int kTileShift = D == 128 ? 4 : 5;
+    static_assert(TK == 1 << kTileShift, "");
+    const int row_shift = min(p.page_shift, kTileShift), page_rows = 1 << row_shift;  // rows of one box
     Cursor pc = piece.c;
     if (ITEMS) pc.i = rank;
     int left = piece.u1 - piece.u0;  // units (items) to come
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(128, 2)
     // The next tile is looked up one step before its loads go out, so that its page numbers are there by then.
     struct Next {
         TileRec rec;
-        int nb, k, page;  // boxes to load; this lane's
+        int nb, k, page;  // boxes to load; this lane's key and table entry
         bool any;
     } nx;
     auto look_up_next = [&]() {
@@ -165,10 +167,10 @@ __global__ void __launch_bounds__(128, 2)
         if (!nx.any) return;
         const int k0 = pc.u.key(pc.i, UK) + warp * TK;
         // boxes that begin below the item's last key; a tile with none completes its phase at once
-        nx.nb = min((pc.u.hi - k0 + page_rows - 1) / page_rows, TK / page_rows);
+        nx.nb = min((pc.u.hi - k0 + page_rows - 1) >> row_shift, TK >> row_shift);
         if (nx.nb < 0 || pc.i >= pc.u.nt) nx.nb = 0;  // ITEMS: a CTA may have no unit of an item
         nx.k = k0 + lane * page_rows;
-        nx.page = lane < nx.nb ? page_of(p, pc.b, nx.k) : 0;
+        if (lane < nx.nb) nx.page = page_entry(p, pc.b, nx.k);
         const bool last = pc.i + CL >= pc.u.nt || (!ITEMS && left == 1);
         const int rows = min(pc.s.m * p.group - pc.rb * R, R);
         nx.rec = TileRec{nx.nb > 0 ? k0 : INT32_MAX, pc.i | (last ? 1 << 24 : 0) | rows << 25, pc.u.nt, pc.u.hi,
@@ -193,8 +195,9 @@ __global__ void __launch_bounds__(128, 2)
         if (lane < now.nb && !skip && !dead) {
             uint8_t* k_dst = ring + st * 2 * C::kTileBytes + lane * page_rows * 128;
             const int row = now.k & ((1 << p.page_shift) - 1);
-            tma_load_5d(k_dst, &tmK, &bar[st], 0, row, 0, now.rec.h, now.page);
-            tma_load_5d(k_dst + C::kTileBytes, &tmV, &bar[st], 0, row, 0, now.rec.h, now.page);
+            const int page = page_of(p, now.page);
+            tma_load_5d(k_dst, &tmK, &bar[st], 0, row, 0, now.rec.h, page);
+            tma_load_5d(k_dst + C::kTileBytes, &tmV, &bar[st], 0, row, 0, now.rec.h, page);
         }
         issued++;
         if (!dead) live = issued;

@@ -332,12 +332,17 @@ __device__ __forceinline__ int cta_of(const Piece& r, int u)
                       : r.more + static_cast<uint32_t>(u - longer) / static_cast<uint32_t>(r.each);
 }
 
-// Page of key k (k below the sequence's length), or a page past the cache's end
-// (which the tensor map fills with zeros) where the table names none of its pages.
-__device__ __forceinline__ int page_of(const PassParams& p, int b, int k)
+// The table's entry for key k (k below the sequence's length), and the page that it
+// stands for: one past the cache's end (which the tensor map fills with zeros) where
+// the table names none of its pages.  Apart, so that an entry can be asked for well
+// before it is looked at.
+__device__ __forceinline__ int page_entry(const PassParams& p, int b, int k)
 {
-    const int pg = __ldg(&p.table[static_cast<int64_t>(b) * p.table_stride + (k >> p.page_shift)]);
-    return pg >= 0 && pg < p.n_pages ? pg : p.n_pages;
+    return __ldg(&p.table[static_cast<int64_t>(b) * p.table_stride + (k >> p.page_shift)]);
+}
+__device__ __forceinline__ int page_of(const PassParams& p, int entry)
+{
+    return entry >= 0 && entry < p.n_pages ? entry : p.n_pages;
 }
 
 __device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3,
