@@ -188,6 +188,136 @@ def test_lengths_beyond_the_table_and_negative():
     assert sa.check_device() == sa.SA_OK
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_len,group", [(1, 4), (1, 6), (3, 8)])
+def test_ragged_batches_cut_over_the_ctas(q_len, group, D):
+    """Long and short sequences in one batch: items cut by several CTAs, items of one unit between them."""
+    kv = [q_len + (9000 * b * b // 1600) % 9001 for b in range(40)]
+    go(Case([q_len] * 40, kv, Hq=2 * group, Hkv=2, D=D, page=32, seed=101), ALL)
+    go(Case([q_len] * 40, kv, Hq=2 * group, Hkv=2, D=D, page=16, seed=102), sa.Pattern(window=3000, sinks=70))
+
+
+def test_more_items_than_clusters():
+    """Whole items by clusters of CTAs, several items one after another."""
+    kv = [3 + (41 * b) % 300 for b in range(90)]
+    go(Case([1] * 90, kv, Hq=8, Hkv=4, D=128, seed=103), sa.Pattern(window=60, sinks=4))
+    go(Case([2] * 150, [n + 2 for n in kv] + [5] * 60, Hq=16, Hkv=4, D=64, seed=104), sa.Pattern(window=40, sinks=1))
+    for heads in (1, 2, 5, 9, 18, 40):  # clusters of eight, four, two, one
+        go(Case([1], [1500], Hq=heads, Hkv=heads, D=64, seed=heads), sa.Pattern(window=900, sinks=2))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_len", [1, 3, 70, 300])
+@pytest.mark.parametrize("prefix", [0, 500])
+def test_infinities_in_places_no_row_sees(q_len, prefix, D):
+    """Keys and values below the window of every row (and behind the sinks) are NaN and infinite."""
+    p = sa.Pattern(window=100, sinks=4)
+    c = Case([q_len, q_len], [1200, 1000], D=D, prefix=prefix, Hq=4, Hkv=2, page=64, seed=111)
+    hidden = lambda n: (4, prefix + n - q_len - 100)  # first and last + 1 of the keys that no row sees
+    for b, n in enumerate(c.kv_len):
+        need = -(-n // c.page)
+        lo, hi = hidden(n)
+        lo, hi = max(lo - prefix, 0), hi - prefix
+        k, v = c.k[b][prefix:].clone(), c.v[b][prefix:].clone()
+        k[lo:hi], v[lo:hi] = math.nan, math.inf
+        c._put(c.table[b, :need].tolist(), k, v)
+        c.k[b], c.v[b] = c.k[b].clone(), c.v[b].clone()
+        c.k[b][4:prefix + hi] = 0  # the plain form multiplies by weights of zero
+        c.v[b][4:prefix + hi] = 0
+    if prefix:
+        k, v = torch.zeros(prefix, 2, D).bfloat16(), torch.zeros(prefix, 2, D).bfloat16()
+        k[:4], v[:4] = c.k[0][:4], c.v[0][:4]
+        k[4:], v[4:] = math.nan, -math.inf
+        c._put(c.prefix_table.tolist(), k, v)
+    go(c, p)
+
+
+def test_table_shares_pages_and_fused_cache():
+    """Two sequences over the same pages; keys and values in one tensor of pages."""
+    c = Case([1, 1, 5], [64, 64, 100], Hq=4, Hkv=2, D=64, page=32, seed=121)
+    c.table[1] = c.table[0]
+    c.k[1], c.v[1] = c.k[0], c.v[0]
+    both = torch.stack([c.k_pages, c.v_pages], 1).cuda()
+    o, lse = sa.fwd_cached(c.dev(c.q), sa.KVCache(both[:, 0], both[:, 1]), c.batch(5), ALL)
+    c.check(o, lse, ALL)
+
+
+def test_no_prefix_is_the_cached_call():
+    c = Case([1, 40], [700, 90], Hq=8, Hkv=2, seed=131)
+    o, l = c.run(WS)
+    o2, l2 = sa.fwd_shared(c.dev(c.q), c.cache(), c.batch(40), None, 0, WS)
+    assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_offsets_beyond_32_bits(D):
+    """Pages that lie more than 2^32 elements into the cache: attention and append."""
+    c = Case([1, 150], [300, 200], Hq=2, Hkv=1, D=D, page=64, seed=141)
+    n = c.k_pages.shape[0]
+    total = (1 << 32) // (64 * D) + 3 * n
+    k, v = (torch.empty((total, 1, 64, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k[-n:], v[-n:] = c.dev(c.k_pages), c.dev(c.v_pages)
+    table = c.table.clone()
+    for b in range(2):
+        need = -(-c.kv_len[b] // 64)
+        table[b, :need] += total - n
+    batch = sa.CacheBatch(c.dev(c.q_start), c.dev(torch.tensor(c.kv_len, dtype=torch.int32)), c.dev(table), max_q=150)
+    cache = sa.KVCache(k, v)
+    o, lse = sa.fwd_cached(c.dev(c.q), cache, batch, ALL)
+    c.check(o, lse, ALL)
+    new = torch.randn(c.T, 1, D, device="cuda").bfloat16()
+    sa.cache_append(new, new, cache, batch)
+    assert torch.equal(k[int(table[0, 299 // 64]), 0, 299 % 64], new[0, 0])
+    assert torch.equal(v[int(table[1, 199 // 64]), 0, 199 % 64], new[150, 0])
+
+
+def test_graphs_of_pieces_and_prefixes_sharing_a_workspace():
+    """Captured calls of both kernels over one workspace, replayed in turn."""
+    a = Case([200, 1, 3], [900, 400, 50], Hq=8, Hkv=2, D=128, page=64, seed=151)
+    b = Case([1] * 30, [9] * 30, Hq=8, Hkv=2, D=128, page=64, prefix=1500, seed=152)
+    need = max(sa.fwd_cached_workspace_bytes(a.T, 8, 2, 128), sa.fwd_shared_workspace_bytes(b.T, 8, 2, 128))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    calls = []
+    for c in (a, b):
+        q, cache, batch, pt = c.dev(c.q), c.cache(), c.batch(max(c.q_len)), c.dev(c.prefix_table)
+        call = (lambda q=q, cache=cache, batch=batch, pt=pt, c=c:
+                sa.fwd_shared(q, cache, batch, pt, c.prefix, ALL, workspace=ws) if c.prefix else
+                sa.fwd_cached(q, cache, batch, ALL, workspace=ws))
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call()
+        calls.append((c, g, out, call))  # the graph reads what the call holds
+    for _ in range(3):
+        for c, g, out, _call in calls:
+            for t in out:
+                t.zero_()
+            g.replay()
+            c.check(*out, ALL)
+
+
+@pytest.mark.parametrize("kind", ["items", "line", "piece", "prefix", "prefix_many"])
+def test_a_wait_that_runs_out(kind):
+    """The bounded waits: a tile that is never loaded sets the status word, and the next call is sound."""
+    c = {"items": lambda: Case([1] * 3, [200, 90, 30], seed=161),
+         "line": lambda: Case([1] * 3, [20000, 90, 30], seed=162),
+         "piece": lambda: Case([1, 300], [200, 900], seed=163),
+         "prefix": lambda: Case([1] * 3, [20, 9, 3], prefix=300, seed=164),
+         "prefix_many": lambda: Case([1] * 40, [20] * 40, prefix=300, seed=165)}[kind]()
+    args = (c.dev(c.q), c.cache(), c.batch(max(c.q_len)))
+    pt = c.dev(c.prefix_table)
+    call = lambda: (sa.fwd_shared(*args, pt, c.prefix, ALL) if c.prefix else sa.fwd_cached(*args, ALL))
+    try:
+        sa.set_debug(sa.DEBUG_SKIP_Q_LOAD, 20_000_000)
+        call()
+        assert sa.check_device() == sa.SA_ERR_DEVICE_TIMEOUT
+    finally:
+        sa.set_debug(0, 0)
+    assert sa.check_device() == sa.SA_OK  # the word was cleared
+    c.check(*call(), ALL)
+
+
 def test_matches_whole_sequence_attention():
     """A prompt appended to an empty cache and attended over it gives what fwd gives."""
     N, Hq, Hkv, D = 700, 4, 2, 128
