@@ -98,6 +98,23 @@ def _sequences(t, st=None) -> _View:
     return _View(t.data_ptr(), st[0], st[1], st[2])
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on ``stream``: taken there, so that what used it before is done by then, and so
+    that a workspace is not handed out again before the kernels are done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _pattern_ref(pattern: Pattern):
+    """The pattern's C structure, made once for a (frozen) pattern."""
+    ref = pattern.__dict__.get("_cached_ref")
+    if ref is None:
+        ref = pattern.__dict__["_cached_ref"] = _ref(pattern._c())
+    return ref
+
+
 def _call(fn, where: str, device, stream, *args) -> None:
     """Call fn(*args, stream handle) with `device` current."""
     index = device.index
@@ -107,7 +124,7 @@ def _call(fn, where: str, device, stream, *args) -> None:
         with torch.cuda.device(device):
             status = fn(*args, _stream_handle(stream, device))
     if status:
-        _check(status, where)
+        _check(status, "sparse_attn_" + where)
 
 
 def _raw_stream(index: int) -> int:
@@ -193,7 +210,7 @@ def _rotate(where, q, k, positions, spec, backward, q_out, k_out, stream):
         raise ValueError(f"{where}: positions must be [{spec.n_axes}, {B} or 1, {N}]")
     qv = _sequences(q, st)
     if q_out is None:
-        q_out = torch.empty(shape, dtype=_BF16, device=dev)
+        q_out = _empty(shape, _BF16, dev, stream)
         ov = _sequences(q_out)
     else:
         oshape, ost = _rows(where, "q_out", q_out, 4, dev)
@@ -208,7 +225,7 @@ def _rotate(where, q, k, positions, spec, backward, q_out, k_out, stream):
         if kshape[0] != B or kshape[2] != N or kshape[3] != D:
             _mismatch(where, "k", kshape, (B, Hkv, N, D))
         if k_out is None:
-            k_out = torch.empty(kshape, dtype=_BF16, device=dev)
+            k_out = _empty(kshape, _BF16, dev, stream)
             okv = _ref(_sequences(k_out))
         else:
             oshape, ost = _rows(where, "k_out", k_out, 4, dev)
@@ -219,7 +236,7 @@ def _rotate(where, q, k, positions, spec, backward, q_out, k_out, stream):
     elif k_out is not None:
         raise ValueError(f"{where}: k_out without k")
     pst = positions.stride()
-    _call(lib.sparse_attn_rotary, "sparse_attn_rotary", dev, stream, _ref(qv), kv, positions.data_ptr(), pst[0],
+    _call(lib.sparse_attn_rotary, "rotary", dev, stream, _ref(qv), kv, positions.data_ptr(), pst[0],
           pst[1] if Bp > 1 else 0, spec._ref, _ref(_Shape(B, Hq, Hkv, N, D)), backward, _ref(ov), okv)
     return q_out, k_out
 
@@ -272,7 +289,7 @@ def cache_append(k, v, cache: KVCache, batch: CacheBatch, rotary: Rotary | None 
         if qshape[0] != T or qshape[2] != cache.D:
             _mismatch(where, "q", qshape, (T, Hq, cache.D))
         if q_out is None:
-            q_out = torch.empty(qshape, dtype=_BF16, device=dev)
+            q_out = _empty(qshape, _BF16, dev, stream)
             ov = _ref(_tokens(q_out))
         else:
             oshape, ost = _rows(where, "q_out", q_out, 3, dev)
@@ -282,28 +299,28 @@ def cache_append(k, v, cache: KVCache, batch: CacheBatch, rotary: Rotary | None 
         qv = _ref(_tokens(q, qst))
     elif q_out is not None:
         raise ValueError(f"{where}: q_out without q")
-    _call(lib.sparse_attn_cache_append, "sparse_attn_cache_append", dev, stream, _ref(_tokens(k, kst)),
+    _call(lib.sparse_attn_cache_append, "cache_append", dev, stream, _ref(_tokens(k, kst)),
           _ref(_tokens(v, vst)), cache._ref, _ref(batch._c(T)), rotary._ref if rotary is not None else None, pos_ptr,
           pos_stride, int(pos_offset), qv, ov, Hq)
     return q_out
 
 
-def _workspace(fn: str, T: int, Hq: int, Hkv: int, D: int) -> int:
+def _workspace(where: str, T: int, Hq: int, Hkv: int, D: int) -> int:
     n = ctypes.c_size_t(0)
+    fn = f"sparse_attn_{where}_workspace"
     _check(getattr(lib, fn)(T, Hq, Hkv, D, ctypes.byref(n)), fn)
     return n.value
 
 
 def fwd_cached_workspace_bytes(T: int, Hq: int, Hkv: int, D: int) -> int:
-    return _workspace("sparse_attn_fwd_cached_workspace", T, Hq, Hkv, D)
+    return _workspace("fwd_cached", T, Hq, Hkv, D)
 
 
 def fwd_shared_workspace_bytes(T: int, Hq: int, Hkv: int, D: int) -> int:
-    return _workspace("sparse_attn_fwd_shared_workspace", T, Hq, Hkv, D)
+    return _workspace("fwd_shared", T, Hq, Hkv, D)
 
 
-def _attend(fn, q, cache, batch, prefix, pattern, scale, out, lse, workspace, stream):
-    where = fn[len("sparse_attn_"):]
+def _attend(fn, where, q, cache, batch, prefix, pattern, scale, out, lse, workspace, stream):
     dev = cache.device
     shape, st = _rows(where, "q", q, 3, dev)
     T, Hq, D = shape
@@ -312,7 +329,7 @@ def _attend(fn, q, cache, batch, prefix, pattern, scale, out, lse, workspace, st
     if batch.device != dev:
         raise TypeError(f"{where}: batch is on {batch.device}, not on {dev}")
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=dev)
+        out = _empty(shape, _BF16, dev, stream)
         ov = _tokens(out)
     else:
         oshape, ost = _rows(where, "out", out, 3, dev)
@@ -320,18 +337,15 @@ def _attend(fn, q, cache, batch, prefix, pattern, scale, out, lse, workspace, st
             _mismatch(where, "out", oshape, shape)
         ov = _tokens(out, ost)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse = _empty((T, Hq), torch.float32, dev, stream)
     elif lse.dtype is not torch.float32 or lse.device != dev or not lse.is_contiguous() or lse.shape != (T, Hq):
         raise TypeError(f"{where}: lse must be a contiguous fp32 tensor [T, Hq] on {dev}")
     if workspace is None:
-        # taken on the stream that uses it, so that it is not handed out again before the kernels are done
-        need = max(_workspace(fn + "_workspace", T, Hq, cache.Hkv, D), 1)
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty(max(_workspace(where, T, Hq, cache.Hkv, D), 1), torch.uint8, dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise TypeError(f"{where}: workspace must be a contiguous tensor on {dev}")
-    _call(getattr(lib, fn), fn, dev, stream, _ref(_tokens(q, st)), cache._ref, _ref(batch._c(T)), *prefix,
-          _ref(pattern._c()), Hq, scale if scale is not None else 1.0 / math.sqrt(D), _ref(ov), lse.data_ptr(),
+    _call(fn, where, dev, stream, _ref(_tokens(q, st)), cache._ref, _ref(batch._c(T)), *prefix,
+          _pattern_ref(pattern), Hq, scale if scale is not None else 1.0 / math.sqrt(D), _ref(ov), lse.data_ptr(),
           workspace.data_ptr(), workspace.nbytes)
     return out, lse
 
@@ -343,7 +357,7 @@ def fwd_cached(q, cache: KVCache, batch: CacheBatch, pattern: Pattern, scale: fl
     ``pattern`` is causal with window, sinks and n_global.  Rows of no sequence keep what ``out``
     and ``lse`` held.  ``workspace``: at least ``fwd_cached_workspace_bytes`` bytes, not shared by
     calls that may run at the same time.  Asynchronous on ``stream``."""
-    return _attend("sparse_attn_fwd_cached", q, cache, batch, (), pattern, scale, out, lse, workspace, stream)
+    return _attend(lib.sparse_attn_fwd_cached, "fwd_cached", q, cache, batch, (), pattern, scale, out, lse, workspace, stream)
 
 
 def fwd_shared(q, cache: KVCache, batch: CacheBatch, prefix_table, prefix_len: int, pattern: Pattern,
@@ -361,5 +375,5 @@ def fwd_shared(q, cache: KVCache, batch: CacheBatch, prefix_table, prefix_len: i
         if prefix_len > prefix_table.shape[0] * cache.page_size:
             raise ValueError("fwd_shared: prefix_table holds fewer than prefix_len tokens")
         ptr = prefix_table.data_ptr()
-    return _attend("sparse_attn_fwd_shared", q, cache, batch, (ptr, prefix_len), pattern, scale, out, lse, workspace,
-                   stream)
+    return _attend(lib.sparse_attn_fwd_shared, "fwd_shared", q, cache, batch, (ptr, prefix_len), pattern, scale, out,
+                   lse, workspace, stream)
