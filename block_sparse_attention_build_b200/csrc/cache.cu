@@ -72,6 +72,31 @@ RotSpec rot_spec(const sa_rotary* r)
     return s;
 }
 
+// A launch that may be set up while the stream's previous kernel still runs; it waits
+// for it where it has to, a call's first kernel at once.  In clusters of `cluster`.
+template <typename... Args>
+int launch_after(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster, const Args&... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    int n = 0;
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+    if (cluster > 1) {
+        at[n].id = cudaLaunchAttributeClusterDimension;
+        at[n].val.clusterDim.x = cluster;
+        at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+        n++;
+    }
+    cfg.attrs = at;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
 template <int D, bool PAGED>
 int rot_launch(const RotSpec& spec, const RotParams& p, bool inter, cudaStream_t st)
 {
@@ -98,8 +123,7 @@ int rot_launch(const RotSpec& spec, const RotParams& p, bool inter, cudaStream_t
     auto kern = layout == kInterleaved ? rotary_kernel<D, kInterleaved, PAGED>
                 : layout == kHalves    ? rotary_kernel<D, kHalves, PAGED>
                                        : rotary_kernel<D, kShuffled, PAGED>;
-    kern<<<grid, kRotThreads, 0, st>>>(spec, pp);
-    return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+    return launch_after(kern, grid, kRotThreads, 0, st, 1, spec, pp);
 }
 
 int page_shift_of(int32_t page_size)
@@ -313,34 +337,6 @@ bool make_map_pages(CUtensorMap* map, const void* base, const sa_kv_cache& c, ui
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A launch that may be set up while the stream's previous kernel, one of this
-// call's, still runs (it waits for it where it has to); in clusters of `cluster`.
-template <typename... Args>
-int launch_after(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool overlap,
-                 int cluster, const Args&... args)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[2];
-    int n = 0;
-    if (overlap) {
-        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[n++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    if (cluster > 1) {
-        at[n].id = cudaLaunchAttributeClusterDimension;
-        at[n].val.clusterDim.x = cluster;
-        at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
-        n++;
-    }
-    cfg.attrs = at;
-    cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
-}
-
 // How decode_kernel runs a pass: in whole items by clusters of `cluster` CTAs
 // (nothing is left to join), or, cluster 0, over the evenly cut line of units.
 struct DecodePlan {
@@ -370,8 +366,7 @@ DecodePlan plan_decode(int64_t keys, int64_t seqs, int64_t rows, int32_t Hkv)
 }
 
 template <int D, int MT, bool ITEMS>
-int launch_decode_as(const sa_kv_cache& cache, const PassParams& p, const DecodePlan& plan, bool overlap,
-                     cudaStream_t st)
+int launch_decode_as(const sa_kv_cache& cache, const PassParams& p, const DecodePlan& plan, cudaStream_t st)
 {
     using C = DecodeCfg<D, MT>;
     auto kern = decode_kernel<D, MT, ITEMS>;
@@ -387,18 +382,18 @@ int launch_decode_as(const sa_kv_cache& cache, const PassParams& p, const Decode
     const uint32_t rows = cache.page_size < C::TK ? cache.page_size : C::TK;
     if (!make_map_pages(&mk, cache.k, cache, rows, D / 64) || !make_map_pages(&mv, cache.v, cache, rows, D / 64))
         return SA_ERR_CUDA;
-    return launch_after(kern, dim3(static_cast<unsigned>(plan.ctas)), C::kThreads, C::kSmemBytes, st, overlap,
+    return launch_after(kern, dim3(static_cast<unsigned>(plan.ctas)), C::kThreads, C::kSmemBytes, st,
                         plan.cluster, mk, mv, p);
 }
 
 template <int D>
-int launch_decode(const sa_kv_cache& cache, const PassParams& p, const DecodePlan& plan, bool overlap, cudaStream_t st)
+int launch_decode(const sa_kv_cache& cache, const PassParams& p, const DecodePlan& plan, cudaStream_t st)
 {
     if (plan.mt == 1)
-        return plan.cluster ? launch_decode_as<D, 1, true>(cache, p, plan, overlap, st)
-                            : launch_decode_as<D, 1, false>(cache, p, plan, overlap, st);
-    return plan.cluster ? launch_decode_as<D, 2, true>(cache, p, plan, overlap, st)
-                        : launch_decode_as<D, 2, false>(cache, p, plan, overlap, st);
+        return plan.cluster ? launch_decode_as<D, 1, true>(cache, p, plan, st)
+                            : launch_decode_as<D, 1, false>(cache, p, plan, st);
+    return plan.cluster ? launch_decode_as<D, 2, true>(cache, p, plan, st)
+                        : launch_decode_as<D, 2, false>(cache, p, plan, st);
 }
 
 template <int D>
@@ -410,11 +405,11 @@ int launch_join(const JoinParams& j, bool prefix, cudaStream_t st)
     const dim3 grid(static_cast<unsigned>(std::min(blocks, 8 * sms)));
     auto kern = few ? (prefix ? join_kernel<D, 8, true> : join_kernel<D, 8, false>)
                     : (prefix ? join_kernel<D, 1, true> : join_kernel<D, 1, false>);
-    return launch_after(kern, grid, 256, 0, st, true, 1, j);
+    return launch_after(kern, grid, 256, 0, st, 1, j);
 }
 
 template <int D>
-int launch_chunk(const sa_kv_cache& cache, const PassParams& p, bool overlap, cudaStream_t st)
+int launch_chunk(const sa_kv_cache& cache, const PassParams& p, cudaStream_t st)
 {
     using C = ChunkCfg<D>;
     auto kern = chunk_kernel<D>;
@@ -434,7 +429,7 @@ int launch_chunk(const sa_kv_cache& cache, const PassParams& p, bool overlap, cu
     const uint32_t rows = cache.page_size < C::UK ? cache.page_size : C::UK;
     if (!make_map_pages(&mk, cache.k, cache, rows, 1) || !make_map_pages(&mv, cache.v, cache, rows, 1))
         return SA_ERR_CUDA;
-    return launch_after(kern, dim3(device_sm_count()), C::kThreads, C::kSmemBytes, st, overlap, 1, mk, mv, p);
+    return launch_after(kern, dim3(device_sm_count()), C::kThreads, C::kSmemBytes, st, 1, mk, mv, p);
 }
 
 // Part arrays and row entries of one pass, from part row `row0` on.
@@ -459,6 +454,7 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
     const bool prefix = p.prefix_len > 0;
     p.rows_above = 0;
     p.rows_upto = INT_MAX;
+    p.first_kernel = 1;
     // most keys of an item, out of `room`: what the window, the sinks and an item's tokens span
     auto most_keys = [&](int64_t room, int64_t tokens) {
         if (p.n_global > 0 || p.window < 0) return p.n_global > 0 ? room : std::min<int64_t>(room, p.cols);
@@ -481,9 +477,9 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
         pp.table_stride = 0;
         use_parts(pp, w, ws, 1, w.rows_decode + w.rows_chunk, D, true);
         if (finished) pp.info = nullptr;
-        if (int rc = all_rows <= kDecodeRows ? launch_decode<D>(cache, pp, over, false, st)
-                                             : launch_chunk<D>(cache, pp, false, st))
+        if (int rc = all_rows <= kDecodeRows ? launch_decode<D>(cache, pp, over, st) : launch_chunk<D>(cache, pp, st))
             return rc;
+        p.first_kernel = 0;
     }
     // each sequence against its own tokens: by decode_kernel alone where no sequence is known to have
     // more than its rows (it can take any), by chunk_kernel alone where there is one sequence of many rows,
@@ -493,11 +489,11 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
             p.pre_acc = reinterpret_cast<const float*>(ws + w.acc[1]);
             p.pre_ml = reinterpret_cast<const float2*>(ws + w.acc_ml[1]);
         }
-        return launch_decode<D>(cache, p, plan, prefix, st);
+        return launch_decode<D>(cache, p, plan, st);
     }
     use_parts(p, w, ws, 0, 0, D, prefix);
     if (rows <= kDecodeRows) {
-        if (int rc = launch_decode<D>(cache, p, plan, prefix, st)) return rc;
+        if (int rc = launch_decode<D>(cache, p, plan, st)) return rc;
         return launch_join<D>(j, prefix, st);
     }
     // Rows are many here, and few of them are cut: without a prefix the CTAs' tail slots are joined instead of
@@ -528,16 +524,16 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
         pp.rows_upto = p.group <= 16 ? 16 : kDecodeRows;
         const DecodePlan line{pp.rows_upto <= 16 ? 1 : 2, 0, kDecodeCtas * int64_t(device_sm_count())};
         use_tails(pp, 0, line.ctas, 16 * line.mt);
-        if (int rc = launch_decode<D>(cache, pp, line, prefix, st)) return rc;
+        if (int rc = launch_decode<D>(cache, pp, line, st)) return rc;
         p.rows_above = pp.rows_upto;
+        p.first_kernel = 0;
     }
-    const bool overlap = prefix || p.B > 1;
     use_parts(p, w, ws, 0, w.rows_decode, D, prefix);
     use_tails(p, 1, device_sm_count(), ChunkCfg<D>::R);
-    if (int rc = launch_chunk<D>(cache, p, overlap, st)) return rc;
+    if (int rc = launch_chunk<D>(cache, p, st)) return rc;
     if (prefix) return launch_join<D>(j, prefix, st);
     const int64_t blocks = (int64_t(tj.entries[0]) + tj.entries[1] + 31) / 32;  // eight threads an entry
-    return launch_after(join_tails_kernel<D>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, true, 1, tj);
+    return launch_after(join_tails_kernel<D>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, 1, tj);
 }
 
 int32_t clip_to(int32_t v, int64_t n) { return v > n ? static_cast<int32_t>(n) : v; }

@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(384, 1)
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
 
+    if (p.first_kernel) wait_previous_kernel();
     launch_dependents();
     if (p.tails != nullptr && threadIdx.x < R) p.tails[blockIdx.x * R + threadIdx.x] = TailRow{0, 0};
     if (threadIdx.x == 64) {

@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(128, 2)
     TileRec* recs = reinterpret_cast<TileRec*>(smem + C::kOffRec) + warp * ST;
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * ST;
 
+    if (p.first_kernel) wait_previous_kernel();
     launch_dependents();
     const SeqView ahead = peek_seq(p);  // on its way while the barriers are set up
     if (lane == 0) {

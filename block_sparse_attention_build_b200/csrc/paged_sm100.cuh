@@ -76,6 +76,7 @@ struct PassParams {
     float2* acc_ml;            // [T, Hq]
     const float* pre_acc;      // not null: what the pass over the prefix left, added to every row
     const float2* pre_ml;
+    int32_t first_kernel;      // 1: the call's first kernel (what came before on the stream is not the call's)
     int32_t* status;
     long long timeout;
     int32_t debug_flags;
@@ -354,11 +355,6 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, uint64_
         "l"(tmap), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
         : "memory");
 }
-
-// Programmatic dependent launch: the next kernel of the stream may be set up now;
-// wait until the previous one's memory is visible.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
 // Joining

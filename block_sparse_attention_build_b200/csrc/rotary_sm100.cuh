@@ -172,6 +172,8 @@ __global__ void __launch_bounds__(kRotThreads, rot_blocks(LAYOUT)) rotary_kernel
         sh_turns[i] = spec.turns[i];
         sh_axis[i] = spec.axis[i];
     }
+    wait_previous_kernel();
+    launch_dependents();
     __syncthreads();
     constexpr int U = rot_unroll(LAYOUT);
     const int h_begin = static_cast<int>(blockIdx.y) * p.heads_per, h_end = h_begin + p.heads_per;
