@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(384, 1)
         tmem_relinquish();
     }
     Piece piece;
-    if (warp == 0) piece = find_piece<R, UK, false>(p, peek_seq(p), blockIdx.x, gridDim.x);
+    if (warp == 0) piece = find_piece<R, UK, false>(p, peek_seq(p), blockIdx.x, gridDim.x, 3);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -195,17 +195,17 @@ __global__ void __launch_bounds__(384, 1)
             constexpr int P = D / 64;  // column panels
             const int box = lane / P, panel = lane % P;
             Cursor c = piece.c;
-            int left = piece.u1 - piece.u0;
+            int left = piece.avail;  // units of the item before the piece's end (which may be more than it has)
             int pos = 0, k_seg = 0;
             for (;; k_seg++) {
                 // describe the segment
                 if (!(ok = wait(&info_empty[k_seg & 1], ((k_seg >> 1) & 1) ^ 1))) break;
-                const int n = left > 0 ? min(c.u.nt - c.i, left) : 0;
+                const int n = left > c.i ? min(c.u.nt, left) - c.i : 0;
                 if (lane == 0) {
                     Segment& g = segs_ring[k_seg & 1];
                     g.n = n;
                     if (n > 0) {
-                        const int u_item = piece.u1 - left - c.i;
+                        const int u_item = piece.u1 - left;  // where the item's units begin on the line
                         g.i = c.i;
                         g.ns = c.u.ns;
                         g.bs = c.u.bs;
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(384, 1)
                         g.h = c.h;
                         g.base = p.prefix_len + c.s.p0;
                         g.begins = u_item >= piece.u0;
-                        g.whole = u_item >= piece.u0 && u_item + c.u.nt <= piece.u1;
+                        g.whole = u_item >= piece.u0 && c.u.nt <= left;
                         g.parts = 0;
                         if (g.begins && !g.whole) g.parts = cta_of(piece, u_item + c.u.nt - 1) - static_cast<int>(blockIdx.x) + 1;
                     }
@@ -250,8 +250,11 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
                 if (!ok) break;
-                left -= n;
-                if (left > 0) next_item<R, UK>(p, piece.pb, c, n_seq);
+                left -= c.u.nt + piece.w;
+                if (left > 0)
+                    next_item<R, UK>(p, piece.pb, c, n_seq);
+                else
+                    left = c.i = 0;
             }
             if (!ok) {
                 if (lane == 0) fail();

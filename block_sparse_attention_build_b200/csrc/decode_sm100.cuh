@@ -90,8 +90,8 @@ __device__ __forceinline__ void cluster_st2(uint32_t addr, uint32_t rank, float2
 // What the loading side of a warp knows about a stage's tile.
 struct alignas(16) TileRec {
     int32_t k0;            // first key of the warp's tile
-    int32_t unit;          // unit of the item (below 2^24), the item's last tile of this CTA (bit 24), its rows (above)
-    int32_t nt;            // the item's units
+    int32_t flags;         // the item's last tile of this CTA (1), its first unit is here (2), all are (4); its rows * 8
+    int32_t parts;         // CTAs that share it (at the last tile, where it begins)
     int32_t hi;            // its keys end before hi
     int32_t first, rb, h;  // the sequence's first token, row block, head
     int32_t base;          // position of the sequence's first new token
@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(128, 2)
     if (!ITEMS && p.tails != nullptr && tid < R) p.tails[blockIdx.x * R + tid] = TailRow{0, 0};
     const int rank = ITEMS ? static_cast<int>(cluster_rank()) : 0;
     const int CL = ITEMS ? static_cast<int>(cluster_size()) : 1;
-    const Piece piece = ITEMS ? find_piece<R, UK, true>(p, ahead, blockIdx.x / CL, gridDim.x / CL)
-                              : find_piece<R, UK, false>(p, ahead, blockIdx.x, gridDim.x);
+    const Piece piece = ITEMS ? find_piece<R, UK, true>(p, ahead, blockIdx.x / CL, gridDim.x / CL, 0)
+                              : find_piece<R, UK, false>(p, ahead, blockIdx.x, gridDim.x, 2);
     const int n_seq = p.over_prefix ? 1 : p.B;
 
     // ---- loads: this warp's tile of every unit of the piece, ST tiles ahead
@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(128, 2)
     const int row_shift = min(p.page_shift, kTileShift), page_rows = 1 << row_shift;  // rows of one box
     Cursor pc = piece.c;
     if (ITEMS) pc.i = rank;
-    int left = piece.u1 - piece.u0;  // units (items) to come
+    // ITEMS: items to come; else units of the item before the piece's end (which may be more than it has)
+    int left = ITEMS ? piece.u1 - piece.u0 : piece.avail;
     int issued = 0, live = 0;  // tiles, and those loaded (a warp whose wait ran out goes on without loads)
     bool dead = false;
     // The next tile is looked up one step before its loads go out, so that its page numbers are there by then.
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(128, 2)
         bool any;
     } nx;
     auto look_up_next = [&]() {
-        nx.any = left > 0;
+        nx.any = ITEMS ? left > 0 : pc.i < left;
         if (!nx.any) return;
         const int k0 = pc.u.key(pc.i, UK) + warp * TK;
         // boxes that begin below the item's last key; a tile with none completes its phase at once
@@ -172,15 +173,25 @@ __global__ void __launch_bounds__(128, 2)
         if (nx.nb < 0 || pc.i >= pc.u.nt) nx.nb = 0;  // ITEMS: a CTA may have no unit of an item
         nx.k = k0 + lane * page_rows;
         if (lane < nx.nb) nx.page = page_entry(p, pc.b, nx.k);
-        const bool last = pc.i + CL >= pc.u.nt || (!ITEMS && left == 1);
+        const bool last = pc.i + CL >= pc.u.nt || (!ITEMS && pc.i + 1 >= left);
         const int rows = min(pc.s.m * p.group - pc.rb * R, R);
-        nx.rec = TileRec{nx.nb > 0 ? k0 : INT32_MAX, pc.i | (last ? 1 << 24 : 0) | rows << 25, pc.u.nt, pc.u.hi,
-                         pc.s.first, pc.rb, pc.h, p.prefix_len + pc.s.p0};
-        if (!ITEMS || last) left--;
+        const int u_item = piece.u1 - left;  // where the item's units begin on the line
+        const bool begins = ITEMS || u_item >= piece.u0, whole = ITEMS || (begins && pc.u.nt <= left);
+        int parts = 0;
+        if (!ITEMS && last && begins && !whole)
+            parts = cta_of(piece, u_item + pc.u.nt - 1) - static_cast<int>(blockIdx.x) + 1;
+        nx.rec = TileRec{nx.nb > 0 ? k0 : INT32_MAX, (last ? 1 : 0) | (begins ? 2 : 0) | (whole ? 4 : 0) | rows << 3,
+                         parts, pc.u.hi, pc.s.first, pc.rb, pc.h, p.prefix_len + pc.s.p0};
+        if (ITEMS && last) left--;
         pc.i += CL;
-        if (pc.i >= pc.u.nt && left > 0) {
-            next_item<R, UK>(p, piece.pb, pc, n_seq);
-            if (ITEMS) pc.i = rank;
+        if (pc.i >= pc.u.nt) {
+            if (!ITEMS) left -= pc.u.nt + piece.w;
+            if (left > 0) {
+                next_item<R, UK>(p, piece.pb, pc, n_seq);
+                if (ITEMS) pc.i = rank;
+            } else {
+                left = 0;
+            }
         }
     };
     auto issue = [&]() {
@@ -229,7 +240,7 @@ __global__ void __launch_bounds__(128, 2)
             fresh = false;
             it = recs[st];
             const int r0 = it.rb * R;
-            rows_left = it.unit >> 25;
+            rows_left = it.flags >> 3;
             const int p_lo = p.over_prefix ? piece.pb.lo : it.base + div_group(p, r0);
             const int p_hi = p.over_prefix ? piece.pb.hi : it.base + div_group(p, r0 + rows_left - 1);
             auto first_seen = [&](int pos) {
@@ -272,9 +283,8 @@ __global__ void __launch_bounds__(128, 2)
         // tiles up to ST ahead: the stage of the last one has just been read
 #pragma unroll 1
         while (issued < j + ST && nx.any) issue();
-        const int k0 = recs[st].k0, packed = recs[st].unit;
-        const int unit = packed & 0xffffff;
-        const bool last = (packed >> 24) & 1;
+        const int k0 = recs[st].k0, flags = recs[st].flags, parts = recs[st].parts;
+        const bool last = flags & 1;
         if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar[st], (j / ST) & 1, p.timeout))) {
             dead = true;
             if (lane == 0) atomicOr(p.status, ST_PAGED_WAIT);
@@ -466,15 +476,12 @@ __global__ void __launch_bounds__(128, 2)
         }
         fresh = true;
 
-        // The item's units are [u_item, u_item + nt); one that is not all in this piece leaves a part.
-        const int u_item = piece.u0 + j - unit;
-        const bool begins = ITEMS || u_item >= piece.u0;
-        const bool whole = ITEMS || (begins && u_item + it.nt <= piece.u1);
+        // An item that is not all in this piece leaves a part.
+        const bool begins = flags & 2, whole = flags & 4;
         const int slot = (2 * static_cast<int>(blockIdx.x) + (begins ? 1 : 0)) * R;
         RowInfo ri{0, 0, 0, 0};
         if (!whole && begins)
-            ri = RowInfo{p.part_row0 + slot, p.part_row0 + slot + R,
-                         cta_of(piece, u_item + it.nt - 1) - static_cast<int>(blockIdx.x) + 1, 2 * R};
+            ri = RowInfo{p.part_row0 + slot, p.part_row0 + slot + R, parts, 2 * R};
         // columns col + 8 i, + 1 of row r; `first` where the row's sum and its entry are to be written too
         auto write = [&](auto n_const, int r, int col, auto& v, float m, float l, bool first) {
             constexpr int N = decltype(n_const)::value;

@@ -17,6 +17,10 @@
 // cut into G pieces of equal length.  So the work is even for any lengths, few
 // rows over a long cache use all SMs, and nothing about it is decided on the
 // host: lengths are read when the kernel runs and a captured graph follows them.
+// An item's start and end take time too (its queries, joining its warps, writing
+// its rows): on the line each item is preceded by `w` places that hold no unit
+// (64 sequences of 34 to 1024 tokens, 8 heads: 1 us a unit, 1.9 us an item; without
+// the places the CTAs' times went from 21 to 39 us).
 // An item that lies inside one piece is finished there.  One that is cut leaves
 // its parts, unnormalised in 32 bits with the rows' running maximum and sum: the
 // CTA in which the item begins writes its part to its "tail" slot, every later one
@@ -220,22 +224,24 @@ struct Piece {
     int G;
     int of_item;     // > 0: that many whole pieces make an item, of item_nt units
     int item_nt;
+    int w;           // places before an item's units
+    int avail;       // units of the item at u0 that lie before u1 (more than it has: the piece goes on)
     PassBounds pb;
     Cursor c;        // at u0 (valid when u0 < u1)
 };
 
 template <int R, int UK, bool ITEMS>
-__device__ __forceinline__ int seq_units(const PassParams& p, const PassBounds& pb, const SeqView& s)
+__device__ __forceinline__ int seq_units(const PassParams& p, const PassBounds& pb, const SeqView& s, int w)
 {
     const int rows = s.m * p.group;
     if (rows == 0 || !takes(p, rows)) return 0;
     const int nrb = (rows + R - 1) / R;
     int n = nrb;
-    if (!ITEMS && p.over_prefix) n = nrb * item_units<R, UK>(p, pb, s, 0).nt;
+    if (!ITEMS && p.over_prefix) n = nrb * (item_units<R, UK>(p, pb, s, 0).nt + w);
     if (!ITEMS && !p.over_prefix) {
         n = 0;
 #pragma unroll 1
-        for (int rb = 0; rb < nrb; rb++) n += item_units<R, UK>(p, pb, s, rb).nt;
+        for (int rb = 0; rb < nrb; rb++) n += item_units<R, UK>(p, pb, s, rb).nt + w;
     }
     return n * p.Hkv;
 }
@@ -266,7 +272,7 @@ __device__ __forceinline__ SeqView peek_seq(const PassParams& p)
 // warp of a CTA finds the same).  It is the first thing every CTA does, and its code runs
 // once: it is kept short, since instructions come from L2 the first time.
 template <int R, int UK, bool ITEMS>
-__device__ __forceinline__ Piece find_piece(const PassParams& p, const SeqView& ahead, int cta, int n_cta)
+__device__ __forceinline__ Piece find_piece(const PassParams& p, const SeqView& ahead, int cta, int n_cta, int w)
 {
     constexpr uint32_t kAll = 0xffffffffu;
     const int lane = threadIdx.x % 32;
@@ -274,15 +280,32 @@ __device__ __forceinline__ Piece find_piece(const PassParams& p, const SeqView& 
     r.pb = PassBounds{0, 0};
     const int n_seq = p.over_prefix ? 1 : p.B;
     if (p.over_prefix) r.pb = pass_bounds(p);
+    // Over the prefix all items have the same units: where they are few, each is cut into as many pieces of
+    // its own as there are CTAs for, so that no CTA pays for the end of one item and the start of another
+    // (8 items of 256 units: two segments took a CTA 48 us, one 40).
+    r.of_item = 0;
+    r.w = w;
+    int items = 0;
+    if (!ITEMS && p.over_prefix) {
+        items = (ahead.m * p.group + R - 1) / R * p.Hkv;
+        if (2 * items <= n_cta && items > 0) r.w = 0;
+    }
     // units of this lane's sequences, and of those before them
     const int per = (n_seq + 31) / 32;
     const int b0 = lane * per, b1 = min(b0 + per, n_seq);
-    int own = 0;
+    int own = 0, own_items = 0;
     SeqView s = ahead;
 #pragma unroll 1
     for (int b = b0; b < b1;) {
-        own += seq_units<R, UK, ITEMS>(p, r.pb, s);
+        own += seq_units<R, UK, ITEMS>(p, r.pb, s, 0);
+        if (!ITEMS) own_items += seq_units<R, UK, true>(p, r.pb, s, 0);
         if (++b < b1) s = load_seq(p, b);
+    }
+    if (!ITEMS) {
+        // places before the items only where the pieces are a few units long: below that a CTA would get a
+        // piece without any
+        if (__reduce_add_sync(kAll, own) < 4 * n_cta) r.w = 0;
+        own += r.w * own_items;
     }
     int incl = own;
 #pragma unroll
@@ -292,26 +315,22 @@ __device__ __forceinline__ Piece find_piece(const PassParams& p, const SeqView& 
     }
     r.U = __shfl_sync(kAll, incl, 31);
     r.G = min(r.U, n_cta);
-    r.u0 = r.u1 = 0;
+    r.u0 = r.u1 = r.avail = r.c.i = 0;
     if (cta >= r.G) return r;
-    // Over the prefix all items have the same units: where they are few, each is cut into as many pieces of
-    // its own as there are CTAs for, so that no CTA pays for the end of one item and the start of another
-    // (8 items of 256 units: two segments took a CTA 48 us, one 40).
-    r.of_item = 0;
     int line = r.U, pieces = r.G, piece = cta, base = 0;
-    if (!ITEMS && p.over_prefix) {
+    if (items > 0 && 2 * items <= n_cta) {
         r.item_nt = item_units<R, UK>(p, r.pb, ahead, 0).nt;
-        const int items = static_cast<uint32_t>(r.U) / static_cast<uint32_t>(r.item_nt);
-        if (2 * items <= n_cta) {
-            r.of_item = min(static_cast<uint32_t>(n_cta) / static_cast<uint32_t>(items), static_cast<uint32_t>(r.item_nt));
-            r.G = items * r.of_item;
-            if (cta >= r.G) return r;
-            const int item = static_cast<uint32_t>(cta) / static_cast<uint32_t>(r.of_item);
-            line = r.item_nt;
-            pieces = r.of_item;
-            piece = cta - item * r.of_item;
-            base = item * r.item_nt;
+        r.of_item = min(static_cast<uint32_t>(n_cta) / static_cast<uint32_t>(items), static_cast<uint32_t>(r.item_nt));
+        r.G = items * r.of_item;
+        if (cta >= r.G) {
+            r.avail = 0;
+            return r;
         }
+        const int item = static_cast<uint32_t>(cta) / static_cast<uint32_t>(r.of_item);
+        line = r.item_nt;
+        pieces = r.of_item;
+        piece = cta - item * r.of_item;
+        base = item * r.item_nt;
     }
     r.each = static_cast<uint32_t>(line) / static_cast<uint32_t>(pieces);
     r.more = line - r.each * pieces;
@@ -324,7 +343,7 @@ __device__ __forceinline__ Piece find_piece(const PassParams& p, const SeqView& 
     if (per > 1 && here) {
 #pragma unroll 1
         for (;; b++) {
-            const int n = seq_units<R, UK, ITEMS>(p, r.pb, load_seq(p, b));
+            const int n = seq_units<R, UK, ITEMS>(p, r.pb, load_seq(p, b), r.w);
             if (r.u0 < at + n) break;
             at += n;
         }
@@ -336,13 +355,15 @@ __device__ __forceinline__ Piece find_piece(const PassParams& p, const SeqView& 
 #pragma unroll 1
     for (;; r.c.rb++) {
         r.c.u = item_units<R, UK>(p, r.pb, r.c.s, r.c.rb);
-        const int n = (ITEMS ? 1 : r.c.u.nt) * p.Hkv;
+        const int n = (ITEMS ? 1 : r.c.u.nt + r.w) * p.Hkv;
         if (r.u0 < at + n) break;
         at += n;
     }
     const uint32_t rest = r.u0 - at;
-    r.c.h = ITEMS ? rest : rest / static_cast<uint32_t>(r.c.u.nt);
-    r.c.i = ITEMS ? 0 : rest - r.c.h * r.c.u.nt;
+    const int place = ITEMS ? 0 : rest % static_cast<uint32_t>(r.c.u.nt + r.w);
+    r.c.h = ITEMS ? rest : rest / static_cast<uint32_t>(r.c.u.nt + r.w);
+    r.c.i = ITEMS ? 0 : max(place - r.w, 0);
+    r.avail = r.u1 - r.u0 + place - r.w;
     return r;
 }
 
