@@ -447,6 +447,25 @@ void use_parts(PassParams& p, const CachedLayout& w, uint8_t* ws, int which, int
 // whose 128-row tiles it fills at least a quarter.
 constexpr int kDecodeRows = 32;
 
+// Most new tokens of a sequence, as far as the host knows.
+int64_t most_new(const PassParams& p, int32_t max_q)
+{
+    return max_q > 0 ? max_q : (int64_t(p.T) + p.B - 1) / p.B;
+}
+
+// The kernels count a pass's units in 31 bits: items times the most units of one, for the kernels that
+// run_paged takes.
+bool units_fit(const PassParams& p, int64_t room, int64_t prefix_len, int32_t max_q)
+{
+    auto fit = [&](int64_t rows, int64_t seqs, int R, int64_t keys, int UK) {
+        return rows / R + seqs <= INT_MAX / (keys / UK + 6) / p.Hkv;
+    };
+    const int64_t all = int64_t(p.T) * p.group;
+    const bool decode = most_new(p, max_q) * p.group <= kDecodeRows;
+    const bool own = decode ? fit(all, p.B, 16, room, 64) : fit(0, p.B, 16, room, 64) && fit(all, p.B, 256, room, 128);
+    return own && (all <= kDecodeRows ? fit(all, 1, 16, prefix_len, 64) : fit(all, 1, 256, prefix_len, 128));
+}
+
 template <int D>
 int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const CachedLayout& w, uint8_t* ws,
               const int32_t* prefix_table, int32_t max_q, cudaStream_t st)
@@ -461,7 +480,7 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
         return std::min<int64_t>(room, int64_t(p.window) + tokens + p.cols);
     };
     const int64_t room = int64_t(p.max_pages) << p.page_shift;
-    const int64_t most_q = max_q > 0 ? max_q : (int64_t(p.T) + p.B - 1) / p.B;
+    const int64_t most_q = most_new(p, max_q);
     const int64_t rows = most_q * p.group, all_rows = int64_t(p.T) * p.group;
     const DecodePlan plan = plan_decode<D>(most_keys(room, most_q), p.B, rows, p.Hkv);
     const DecodePlan over = plan_decode<D>(p.prefix_len, 1, all_rows, p.Hkv);
@@ -554,6 +573,13 @@ int fwd_paged(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* 
     if (cache->Hkv == 0 || cache->n_pages == 0 || Hq % cache->Hkv) return SA_ERR_UNSUPPORTED;
     if (int64_t(T) * Hq > INT_MAX / 2) return SA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
     if (prefix_len > 0 && !prefix_table) return SA_ERR_INVALID_ARG;
+    PassParams p{};
+    p.B = batch->B;
+    p.T = T;
+    p.Hq = Hq;
+    p.Hkv = cache->Hkv;
+    p.group = Hq / cache->Hkv;
+    if (!units_fit(p, int64_t(batch->max_pages) * cache->page_size, prefix_len, batch->max_q)) return SA_ERR_UNSUPPORTED;
     if (int rc = view_status(q, 1, Hq, T, false)) return rc;
     if (int rc = view_status(o, 1, Hq, T, true)) return rc;
     if (!lse || !workspace) return SA_ERR_INVALID_ARG;
@@ -567,7 +593,6 @@ int fwd_paged(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* 
     int32_t* status = nullptr;
     if (int rc = device_status_word(&status)) return rc;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    PassParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q->data);
     p.q_token = T > 1 ? q->token_stride : 0;
     p.q_head = Hq > 1 ? q->head_stride : 0;
@@ -579,14 +604,6 @@ int fwd_paged(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* 
     p.kv_len = batch->kv_len;
     p.table = batch->table;
     p.table_stride = batch->B > 1 ? batch->table_stride : 0;
-    p.B = batch->B;
-    p.T = T;
-    p.Hq = Hq;
-    p.Hkv = cache->Hkv;
-    p.group = Hq / cache->Hkv;
-    // the kernels count units of 64 keys or more of 16 rows or more in 31 bits
-    const int64_t most = std::max<int64_t>(int64_t(batch->max_pages) * cache->page_size, prefix_len) / 64 + 3;
-    if ((int64_t(T) * p.group / 16 + batch->B) * most > INT_MAX / int64_t(p.Hkv)) return SA_ERR_UNSUPPORTED;
     while ((int64_t(1) << p.group_shift) < p.group) p.group_shift++;
     p.group_shift += 31;
     p.group_mul = static_cast<uint32_t>((uint64_t(1) << p.group_shift) / p.group + 1);

@@ -415,7 +415,8 @@ typedef struct {
  * Host arrays, read before the call returns: freq [n_pairs] finite radians per
  * position, axis [n_pairs] in [0, n_axes), or NULL for axis 0 throughout.
  * 0 <= 2 n_pairs <= D, 1 <= n_axes <= 4, interleaved 0 or 1 (else
- * SA_ERR_INVALID_ARG).
+ * SA_ERR_INVALID_ARG).  Frequencies are kept modulo a turn per position, to 2^-64
+ * of it.
  */
 typedef struct {
     int32_t n_pairs, n_axes, interleaved;
@@ -515,8 +516,17 @@ int sparse_attn_fwd_shared_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t
  *         256-byte aligned (SA_ERR_MISALIGNED; SA_ERR_BUFFER_TOO_SMALL), contents
  *         need not be preserved; not shared by calls that may run at the same time
  * Asynchronous on `stream`; errors as sparse_attn_fwd.  What the cache holds at
- * places no row of a sequence sees (infinities and NaN too) does not matter.
- * Results of the same call on the same inputs are bit-identical.
+ * places no row of a sequence sees (infinities and NaN too) does not matter; an
+ * infinity or NaN in a value that one row of a sequence sees may reach the
+ * sequence's other rows (over a shared prefix: any row) through weights of zero.
+ * Weights are rounded to bf16 for the product with V; scores, maxima, sums, the
+ * LSE and partial results are held in 32 bits.  Results of the same call on the
+ * same inputs are bit-identical.
+ * Supported: D in {64, 128}, Hq % Hkv == 0, T * Hq below 2^30, and row blocks times
+ * key blocks of all sequences and heads (as blocks of 256 rows and 128 keys, or of 16
+ * and 64 where sequences have few rows, counted over the table's room) below 2^31;
+ * else SA_ERR_UNSUPPORTED.  The wait limit and the first hook of
+ * sparse_attn_set_debug (here: a tile of keys is not loaded) apply too.
  */
 int sparse_attn_fwd_cached(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* batch,
                            const sa_pattern* pattern, int32_t Hq, float scale, const sa_view* o, float* lse,

@@ -128,6 +128,9 @@ def test_attention_refusals(shared):
     assert call(Hq=3) == UNS
     assert call(Hq=-1) == INV
     assert call(cache=cache_of(Hkv=0)) == UNS
+    assert call(batch=batch_of(T=2 ** 29)) == UNS             # rows are counted in 31 bits
+    big = dict(B=1, T=2 ** 22, max_q=2 ** 22, max_pages=2 ** 25, stride=2 ** 25)
+    assert call(batch=batch_of(**big)) == UNS                 # and so are units of rows and keys
     assert call(q=view(ptr=None)) == INV
     assert call(o=view(ptr=OK_PTR + 4)) == MIS
     assert call(o=view(t=0)) == INV
