@@ -13,10 +13,11 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
-from . import EXPORTED, Pattern, _check, _Pattern, _Shape, _stream_handle, lib
+from . import EXPORTED, Pattern, _check, _Pattern, _stream_handle, lib
 
 
 class _View(ctypes.Structure):
@@ -43,8 +44,9 @@ class _CacheBatch(ctypes.Structure):
 
 def _declare() -> None:
     i32, i64, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
-    V, C, B = ctypes.POINTER(_View), ctypes.POINTER(_KVCache), ctypes.POINTER(_CacheBatch)
-    R, P, S = ctypes.POINTER(_Rotary), ctypes.POINTER(_Pattern), ctypes.POINTER(_Shape)
+    # views, batches and shapes are made for every call: as packed bytes, whose address is passed
+    V = B = S = vp
+    C, R, P = ctypes.POINTER(_KVCache), ctypes.POINTER(_Rotary), ctypes.POINTER(_Pattern)
     lib.sparse_attn_rotary.argtypes = [V, V, vp, i64, i64, R, S, i32, V, V, vp]
     lib.sparse_attn_cache_append.argtypes = [V, V, C, B, R, vp, i64, i32, V, V, i32, vp]
     lib.sparse_attn_fwd_cached.argtypes = [V, C, B, P, i32, ctypes.c_float, V, vp, vp, sz, vp]
@@ -86,16 +88,22 @@ def _mismatch(where: str, name: str, shape, want):
     raise ValueError(f"{where}: {name} has the shape {tuple(shape)}, not {tuple(want)}")
 
 
-def _tokens(t, st=None) -> _View:
+# The C structures made for every call, packed (half the time of a ctypes structure).
+_pack_view = struct.Struct("@Pqqq").pack      # _View
+_pack_shape = struct.Struct("@5i").pack       # _Shape
+_pack_batch = struct.Struct("@4iqPPP").pack   # _CacheBatch
+
+
+def _tokens(t, st=None) -> bytes:
     """View of a tensor of tokens [T, H, D]."""
     st = st or t.stride()
-    return _View(t.data_ptr(), 0, st[1], st[0])
+    return _pack_view(t.data_ptr(), 0, st[1], st[0])
 
 
-def _sequences(t, st=None) -> _View:
+def _sequences(t, st=None) -> bytes:
     """View of whole sequences [B, H, N, D]."""
     st = st or t.stride()
-    return _View(t.data_ptr(), st[0], st[1], st[2])
+    return _pack_view(t.data_ptr(), st[0], st[1], st[2])
 
 
 def _empty(shape, dtype, device, stream):
@@ -191,13 +199,12 @@ class CacheBatch:
         if q_start.shape[0] != B + 1 or table.shape[0] != B:
             raise ValueError("CacheBatch: q_start [B + 1], kv_len [B] and table [B, max_pages] disagree on B")
         self.q_start, self.kv_len, self.table, self.max_q, self.device = q_start, kv_len, table, max_q, dev
-        self._struct = _CacheBatch(B, 0, max_q or 0, table.shape[1], table.stride(0) if B > 1 else table.shape[1],
-                                   q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr())
+        self._B = B
+        self._rest = (max_q or 0, table.shape[1], table.stride(0) if B > 1 else table.shape[1], q_start.data_ptr(),
+                      kv_len.data_ptr(), table.data_ptr())
 
-    def _c(self, T: int) -> _CacheBatch:
-        s = _CacheBatch.from_buffer_copy(self._struct)
-        s.T = T
-        return s
+    def _c(self, T: int) -> bytes:
+        return _pack_batch(self._B, T, *self._rest)
 
 
 def _rotate(where, q, k, positions, spec, backward, q_out, k_out, stream):
@@ -226,18 +233,18 @@ def _rotate(where, q, k, positions, spec, backward, q_out, k_out, stream):
             _mismatch(where, "k", kshape, (B, Hkv, N, D))
         if k_out is None:
             k_out = _empty(kshape, _BF16, dev, stream)
-            okv = _ref(_sequences(k_out))
+            okv = _sequences(k_out)
         else:
             oshape, ost = _rows(where, "k_out", k_out, 4, dev)
             if oshape != kshape:
                 _mismatch(where, "k_out", oshape, kshape)
-            okv = _ref(_sequences(k_out, ost))
-        kv = _ref(_sequences(k, kst))
+            okv = _sequences(k_out, ost)
+        kv = _sequences(k, kst)
     elif k_out is not None:
         raise ValueError(f"{where}: k_out without k")
     pst = positions.stride()
-    _call(lib.sparse_attn_rotary, "rotary", dev, stream, _ref(qv), kv, positions.data_ptr(), pst[0],
-          pst[1] if Bp > 1 else 0, spec._ref, _ref(_Shape(B, Hq, Hkv, N, D)), backward, _ref(ov), okv)
+    _call(lib.sparse_attn_rotary, "rotary", dev, stream, qv, kv, positions.data_ptr(), pst[0],
+          pst[1] if Bp > 1 else 0, spec._ref, _pack_shape(B, Hq, Hkv, N, D), backward, ov, okv)
     return q_out, k_out
 
 
@@ -290,17 +297,17 @@ def cache_append(k, v, cache: KVCache, batch: CacheBatch, rotary: Rotary | None 
             _mismatch(where, "q", qshape, (T, Hq, cache.D))
         if q_out is None:
             q_out = _empty(qshape, _BF16, dev, stream)
-            ov = _ref(_tokens(q_out))
+            ov = _tokens(q_out)
         else:
             oshape, ost = _rows(where, "q_out", q_out, 3, dev)
             if oshape != qshape:
                 _mismatch(where, "q_out", oshape, qshape)
-            ov = _ref(_tokens(q_out, ost))
-        qv = _ref(_tokens(q, qst))
+            ov = _tokens(q_out, ost)
+        qv = _tokens(q, qst)
     elif q_out is not None:
         raise ValueError(f"{where}: q_out without q")
-    _call(lib.sparse_attn_cache_append, "cache_append", dev, stream, _ref(_tokens(k, kst)),
-          _ref(_tokens(v, vst)), cache._ref, _ref(batch._c(T)), rotary._ref if rotary is not None else None, pos_ptr,
+    _call(lib.sparse_attn_cache_append, "cache_append", dev, stream, _tokens(k, kst),
+          _tokens(v, vst), cache._ref, batch._c(T), rotary._ref if rotary is not None else None, pos_ptr,
           pos_stride, int(pos_offset), qv, ov, Hq)
     return q_out
 
@@ -344,8 +351,8 @@ def _attend(fn, where, q, cache, batch, prefix, pattern, scale, out, lse, worksp
         workspace = _empty(max(_workspace(where, T, Hq, cache.Hkv, D), 1), torch.uint8, dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise TypeError(f"{where}: workspace must be a contiguous tensor on {dev}")
-    _call(fn, where, dev, stream, _ref(_tokens(q, st)), cache._ref, _ref(batch._c(T)), *prefix,
-          _pattern_ref(pattern), Hq, scale if scale is not None else 1.0 / math.sqrt(D), _ref(ov), lse.data_ptr(),
+    _call(fn, where, dev, stream, _tokens(q, st), cache._ref, batch._c(T), *prefix,
+          _pattern_ref(pattern), Hq, scale if scale is not None else 1.0 / math.sqrt(D), ov, lse.data_ptr(),
           workspace.data_ptr(), workspace.nbytes)
     return out, lse
 

@@ -63,10 +63,12 @@ RotSpec rot_spec(const sa_rotary* r)
     if (!r) return s;
     s.n_pairs = r->n_pairs;
     for (int i = 0; i < r->n_pairs; i++) {
-        // freq / 2 pi modulo 1 as a 64-bit fraction (whole turns drop out: positions are whole numbers)
-        const long double turns = static_cast<long double>(r->freq[i]) / 6.283185307179586476925286766559005768L;
-        const long double frac = turns - floorl(turns);
-        s.turns[i] = frac >= 1.0L ? 0 : static_cast<uint64_t>(frac * 18446744073709551616.0L);
+        // freq / 2 pi modulo 1 as a 64-bit fraction, whose low bit stays 0 (whole turns drop out: positions are
+        // whole numbers).  Done for every call, so without a division or a call of floor.
+        long double turns = static_cast<long double>(r->freq[i]) * 0.159154943091895335768883763372514362L;
+        if (fabsl(turns) >= 0x1p62L) turns = fmodl(turns, 1.0L);
+        const long double frac = turns - static_cast<long double>(static_cast<int64_t>(turns));  // in (-1, 1)
+        s.turns[i] = static_cast<uint64_t>(static_cast<int64_t>(frac * 0x1p63L)) << 1;
         s.axis[i] = static_cast<uint8_t>(r->axis ? r->axis[i] : 0);
     }
     return s;

@@ -415,7 +415,7 @@ typedef struct {
  * Host arrays, read before the call returns: freq [n_pairs] finite radians per
  * position, axis [n_pairs] in [0, n_axes), or NULL for axis 0 throughout.
  * 0 <= 2 n_pairs <= D, 1 <= n_axes <= 4, interleaved 0 or 1 (else
- * SA_ERR_INVALID_ARG).  Frequencies are kept modulo a turn per position, to 2^-64
+ * SA_ERR_INVALID_ARG).  Frequencies are kept modulo a turn per position, to 2^-63
  * of it.
  */
 typedef struct {

@@ -86,6 +86,18 @@ def test_rotary_far_positions_and_values_it_keeps():
     assert bool(((y[..., :48].double() - z).abs() <= 2.0 ** -8 * z.abs() + 2.0 ** -19 * size).all())
 
 
+def test_rotary_frequencies_of_any_size():
+    """Negative frequencies, whole and many turns a position, and none."""
+    freq = [-1.0, 2 * math.pi, -2 * math.pi, 100.0, -12345.678, 1e9, 0.0, 1e-12]
+    spec = sa.Rotary(freq)
+    q = torch.randn(1, 3, 5, 64, device="cuda").bfloat16()
+    pos = torch.tensor([0, 1, -3, 77, 12], dtype=torch.int32, device="cuda").expand(1, 1, 5).contiguous()
+    y, _ = sa.rotary(q, None, pos, spec)
+    z, size = plain(q, pos[:, :, None], freq, [0] * 8, False)
+    # both sides reduce 1e9 x 77 radians from 64 bits: 2^-53 of that, 2^-17 radians
+    assert bool(((y.double() - z).abs() <= 2.0 ** -8 * z.abs() + 2.0 ** -15 * size).all())
+
+
 def test_rotary_gradient_against_differences():
     """<R x, y> differentiates to R^T y: the backward call against differences of the forward in 64 bits."""
     freq, axis, spec = spec_of(30, 3, False)
