@@ -347,15 +347,15 @@ struct DecodePlan {
     int64_t ctas;
 };
 
-// keys: most keys of an item, seqs: sequences, rows: most rows of one, as far as the host knows.
+// keys: most keys of an item, seqs: sequences, rows: most rows of one, as far as the host knows; held: CTAs
+// that have room at once.
 // Whole items where each CTA then has at most six units: the cut is even for any lengths, but its join
 // costs a launch and some 3 us.
 template <int D>
-DecodePlan plan_decode(int64_t keys, int64_t seqs, int64_t rows, int32_t Hkv)
+DecodePlan plan_decode(int64_t keys, int64_t seqs, int64_t rows, int32_t Hkv, int64_t held)
 {
     DecodePlan d;
     d.mt = rows <= 16 ? 1 : 2;
-    const int64_t held = kDecodeCtas * int64_t(device_sm_count());
     const int64_t items = seqs * Hkv * ((rows + 16 * d.mt - 1) / (16 * d.mt));
     const int64_t units = keys / DecodeCfg<D, 1>::UK + 3;  // the sinks' and the band's last and first may be partly used
     int64_t c = 1;
@@ -363,7 +363,7 @@ DecodePlan plan_decode(int64_t keys, int64_t seqs, int64_t rows, int32_t Hkv)
     const bool whole = (units + c - 1) / c <= 6 && items * c <= 4 * held;
     d.cluster = whole ? static_cast<int>(c) : 0;
     const int64_t clusters = items < held / c ? items : held / c;
-    d.ctas = whole ? clusters * c : held;
+    d.ctas = whole ? clusters * c : kDecodeCtas * int64_t(device_sm_count());
     return d;
 }
 
@@ -484,8 +484,11 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
     const int64_t room = int64_t(p.max_pages) << p.page_shift;
     const int64_t most_q = most_new(p, max_q);
     const int64_t rows = most_q * p.group, all_rows = int64_t(p.T) * p.group;
-    const DecodePlan plan = plan_decode<D>(most_keys(room, most_q), p.B, rows, p.Hkv);
-    const DecodePlan over = plan_decode<D>(p.prefix_len, 1, all_rows, p.Hkv);
+    const int64_t held = kDecodeCtas * int64_t(device_sm_count());
+    const DecodePlan over = plan_decode<D>(p.prefix_len, 1, all_rows, p.Hkv, held);
+    // whole items of the sequences run beside those of the prefix, for whose rows they wait at their ends
+    const int64_t beside = prefix && all_rows <= kDecodeRows && over.cluster > 0 ? std::max<int64_t>(held - over.ctas, 1) : held;
+    const DecodePlan plan = plan_decode<D>(most_keys(room, most_q), p.B, rows, p.Hkv, beside);
     // Nothing is left for join_kernel where each item is finished by its CTAs; over a prefix the sequences'
     // pass then adds what the prefix's left.
     const bool finished = rows <= kDecodeRows && plan.cluster > 0 &&
