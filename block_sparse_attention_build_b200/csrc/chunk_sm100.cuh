@@ -131,9 +131,6 @@ __global__ void __launch_bounds__(384, 1)
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
 
-    if (p.first_kernel) wait_previous_kernel();
-    launch_dependents();
-    if (p.tails != nullptr && threadIdx.x < R) p.tails[blockIdx.x * R + threadIdx.x] = TailRow{0, 0};
     if (threadIdx.x == 64) {
         for (int i = 0; i < S; i++) {
             mbar_init(&ring_full[i], 1);
@@ -157,6 +154,13 @@ __global__ void __launch_bounds__(384, 1)
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
     }
+    if (threadIdx.x == 96) {
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    if (p.first_kernel) wait_previous_kernel();
+    launch_dependents();
+    if (p.tails != nullptr && threadIdx.x < R) p.tails[blockIdx.x * R + threadIdx.x] = TailRow{0, 0};
     Piece piece;
     if (warp == 0) piece = find_piece<R, UK, false>(p, peek_seq(p), blockIdx.x, gridDim.x, 3);
     tc_fence_before_sync();

@@ -132,14 +132,17 @@ __global__ void __launch_bounds__(128, 2)
     TileRec* recs = reinterpret_cast<TileRec*>(smem + C::kOffRec) + warp * ST;
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * ST;
 
-    if (p.first_kernel) wait_previous_kernel();
-    launch_dependents();
-    const SeqView ahead = peek_seq(p);  // on its way while the barriers are set up
+    // what needs nothing of the kernel before: barriers, the tensor maps' way into the cache
     if (lane == 0) {
         for (int s = 0; s < ST; s++) mbar_init(&bar[s], 1);
         fence_barrier_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
     }
     __syncwarp();
+    if (p.first_kernel) wait_previous_kernel();
+    launch_dependents();
+    const SeqView ahead = peek_seq(p);
     // no tail rows yet (a segment's end, where there may be some, lies behind barriers)
     if (!ITEMS && p.tails != nullptr && tid < R) p.tails[blockIdx.x * R + tid] = TailRow{0, 0};
     const int rank = ITEMS ? static_cast<int>(cluster_rank()) : 0;
