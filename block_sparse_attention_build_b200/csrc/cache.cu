@@ -520,10 +520,13 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
         if (int rc = launch_decode<D>(cache, p, plan, st)) return rc;
         return launch_join<D>(j, prefix, st);
     }
-    // Rows are many here, and few of them are cut: without a prefix the CTAs' tail slots are joined instead of
-    // looking at every row (4.6 thousand tokens of 32 heads: 25 us for that).
+    // Rows may be many here, and few of them cut: then, without a prefix, the CTAs' tail slots are joined instead
+    // of looking at every row (4.6 thousand tokens of 32 heads: 25 us for that).
+    // Up to 16 thousand rows every row is looked at: the slots of all CTAs are 42 thousand entries whatever the batch
+    // (517 tokens of 4 heads: 29 us by slots, 23 by rows; 2988 of 32 heads: 44 and 53).
+    const bool by_tails = !prefix && int64_t(p.T) * p.Hq > 16384;
     TailJoinParams tj{};
-    if (!prefix) {
+    if (by_tails) {
         tj.part_o = j.part_o;
         tj.part_ml = j.part_ml;
         tj.o = j.o;
@@ -535,7 +538,7 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
         tj.part_rows = j.part_rows;
     }
     auto use_tails = [&](PassParams& pp, int which, int64_t ctas, int R) {
-        if (prefix) return;
+        if (!by_tails) return;
         pp.info = nullptr;
         pp.tails = reinterpret_cast<TailRow*>(ws + w.tails[which]);
         tj.tails[which] = pp.tails;
@@ -555,7 +558,7 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
     use_parts(p, w, ws, 0, w.rows_decode, D, prefix);
     use_tails(p, 1, device_sm_count(), ChunkCfg<D>::R);
     if (int rc = launch_chunk<D>(cache, p, st)) return rc;
-    if (prefix) return launch_join<D>(j, prefix, st);
+    if (!by_tails) return launch_join<D>(j, prefix, st);
     const int64_t blocks = (int64_t(tj.entries[0]) + tj.entries[1] + 31) / 32;  // eight threads an entry
     return launch_after(join_tails_kernel<D>, dim3(static_cast<unsigned>(blocks)), 256, 0, st, 1, tj);
 }
