@@ -17,7 +17,7 @@ import struct
 
 import torch
 
-from . import EXPORTED, Pattern, _check, _Pattern, _stream_handle, lib
+from . import EXPORTED, Pattern, _check, _stream_handle, lib
 
 
 class _View(ctypes.Structure):
@@ -44,9 +44,9 @@ class _CacheBatch(ctypes.Structure):
 
 def _declare() -> None:
     i32, i64, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
-    # views, batches and shapes are made for every call: as packed bytes, whose address is passed
-    V = B = S = vp
-    C, R, P = ctypes.POINTER(_KVCache), ctypes.POINTER(_Rotary), ctypes.POINTER(_Pattern)
+    # views, batches, patterns and shapes are made for every call: as packed bytes, whose address is passed
+    V = B = S = P = vp
+    C, R = ctypes.POINTER(_KVCache), ctypes.POINTER(_Rotary)
     lib.sparse_attn_rotary.argtypes = [V, V, vp, i64, i64, R, S, i32, V, V, vp]
     lib.sparse_attn_cache_append.argtypes = [V, V, C, B, R, vp, i64, i32, V, V, i32, vp]
     lib.sparse_attn_fwd_cached.argtypes = [V, C, B, P, i32, ctypes.c_float, V, vp, vp, sz, vp]
@@ -91,6 +91,7 @@ def _mismatch(where: str, name: str, shape, want):
 # The C structures made for every call, packed (half the time of a ctypes structure).
 _pack_view = struct.Struct("@Pqqq").pack      # _View
 _pack_shape = struct.Struct("@5i").pack       # _Shape
+_pack_pattern = struct.Struct("@7i").pack    # _Pattern
 _pack_batch = struct.Struct("@4iqPPP").pack   # _CacheBatch
 
 
@@ -113,14 +114,6 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _pattern_ref(pattern: Pattern):
-    """The pattern's C structure, made once for a (frozen) pattern."""
-    ref = pattern.__dict__.get("_cached_ref")
-    if ref is None:
-        ref = pattern.__dict__["_cached_ref"] = _ref(pattern._c())
-    return ref
 
 
 def _call(fn, where: str, device, stream, *args) -> None:
@@ -328,7 +321,7 @@ def fwd_shared_workspace_bytes(T: int, Hq: int, Hkv: int, D: int) -> int:
 
 
 def _attend(fn, where, q, cache, batch, prefix, pattern, scale, out, lse, workspace, stream):
-    dev = cache.device
+    dev, p = cache.device, pattern
     shape, st = _rows(where, "q", q, 3, dev)
     T, Hq, D = shape
     if D != cache.D:
@@ -352,7 +345,7 @@ def _attend(fn, where, q, cache, batch, prefix, pattern, scale, out, lse, worksp
     elif workspace.device != dev or not workspace.is_contiguous():
         raise TypeError(f"{where}: workspace must be a contiguous tensor on {dev}")
     _call(fn, where, dev, stream, _tokens(q, st), cache._ref, batch._c(T), *prefix,
-          _pattern_ref(pattern), Hq, scale if scale is not None else 1.0 / math.sqrt(D), ov, lse.data_ptr(),
+          _pack_pattern(p.causal, p.window, p.sinks, p.stride, p.n_global, p.area, p.summary), Hq, scale if scale is not None else 1.0 / math.sqrt(D), ov, lse.data_ptr(),
           workspace.data_ptr(), workspace.nbytes)
     return out, lse
 

@@ -745,4 +745,4 @@ extern "C" const char* sparse_attn_status_string(int status)
     }
 }
 
-extern "C" int32_t sparse_attn_version(void) { return 300; }
+extern "C" int32_t sparse_attn_version(void) { return 400; }

@@ -171,3 +171,13 @@ def test_binding_refuses_host_and_wrong_tensors():
         sa.Rotary([1.0, 2.0], axis=[0])
     with pytest.raises(TypeError, match="bf16 CUDA"):
         sa.rotary(x, x, torch.zeros(1, 1, 16, dtype=torch.int32), sa.Rotary([1.0]))
+
+
+def test_packed_structures_match_the_header():
+    """The structures packed for every call lay their fields out as the ctypes ones do."""
+    b = cc._CacheBatch(2, 3, 4, 5, 6, 7, 8, 9)
+    assert bytes(b) == cc._pack_batch(2, 3, 4, 5, 6, 7, 8, 9)
+    assert bytes(cc._View(1, 2, 3, 4)) == cc._pack_view(1, 2, 3, 4)
+    assert bytes(sa._Shape(1, 2, 3, 4, 5)) == cc._pack_shape(1, 2, 3, 4, 5)
+    p = sa.Pattern(window=5, sinks=2, n_global=3)
+    assert bytes(p._c()) == cc._pack_pattern(p.causal, p.window, p.sinks, p.stride, p.n_global, p.area, p.summary)
