@@ -289,7 +289,8 @@ CachedLayout cached_layout(int32_t T, int32_t Hq, int32_t D, bool prefix)
     CachedLayout w{};
     w.rows_decode = 2 * int64_t(kDecodeCtas) * n_sm * 32;
     w.rows_chunk = 2 * int64_t(n_sm) * 256;
-    // the sequences' own pass may take both kernels, that over the prefix takes one
+    // the sequences' own pass may take both kernels, that over the prefix takes one; where decode_kernel's warps
+    // each have a piece it runs alone, and their 2 x 4 x 2 n_sm x 16 rows lie in both kernels'
     w.part_rows = w.rows_decode + w.rows_chunk + (prefix ? w.rows_chunk : 0);
     const size_t th = size_t(T) * Hq;
     size_t at = 0;
@@ -339,39 +340,49 @@ bool make_map_pages(CUtensorMap* map, const void* base, const sa_kv_cache& c, ui
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How decode_kernel runs a pass: in whole items by clusters of `cluster` CTAs
-// (nothing is left to join), or, cluster 0, over the evenly cut line of units.
+// How decode_kernel runs a pass (see its modes; in kClusters nothing is left to join).
 struct DecodePlan {
     int mt;       // rows of an item: 16 or 32
-    int cluster;
+    DecodeMode mode;
+    int cluster;  // CTAs of a cluster
     int64_t ctas;
 };
 
 // keys: most keys of an item, seqs: sequences, rows: most rows of one, as far as the host knows; held: CTAs
 // that have room at once.
-// Whole items where each CTA then has at most six units: the cut is even for any lengths, but its join
-// costs a launch and some 3 us.
+// Whole items by clusters where each CTA then has at most six units: the cut is even for any lengths, but
+// its join costs a launch and some 3 us.  The line by warps (`by_warps`: it may be) where there is an item or
+// more to every CTA and none has many keys: 256 sequences of up to 256 keys and 8 heads of 128, 40.8 us by CTAs
+// and 28.3 by warps, 500 of up to 500, 91.8 and 71.9, 300 of up to 1000, 80.9 and 75.7, 256 of up to 2048, 110
+// and 116; below one item to a CTA there is nothing in it.  Items of up to 128 keys are whole to a CTA each
+// until there are two to every CTA (64 sequences of up to 60: 9.3 us, by warps 11.3; 80 of up to 100: 14.9, 13.1).
 template <int D>
-DecodePlan plan_decode(int64_t keys, int64_t seqs, int64_t rows, int32_t Hkv, int64_t held)
+DecodePlan plan_decode(int64_t keys, int64_t seqs, int64_t rows, int32_t Hkv, int64_t held, bool by_warps)
 {
     DecodePlan d;
     d.mt = rows <= 16 ? 1 : 2;
     const int64_t items = seqs * Hkv * ((rows + 16 * d.mt - 1) / (16 * d.mt));
-    const int64_t units = keys / DecodeCfg<D, 1>::UK + 3;  // the sinks' and the band's last and first may be partly used
+    const int64_t units = keys / DecodeCfg<D, 1>::UK + 3;  // the sinks' and the band's first and last may be part full
+    d.cluster = 1;
+    if (by_warps && d.mt == 1 && items >= held && keys <= 1024 && (keys > 128 || items >= 2 * held)) {
+        d.mode = kWarps;
+        d.ctas = held;
+        return d;
+    }
     int64_t c = 1;
     while (c < 8 && items * c * 2 <= held && c < units) c *= 2;
     const bool whole = (units + c - 1) / c <= 6 && items * c <= 4 * held;
-    d.cluster = whole ? static_cast<int>(c) : 0;
-    const int64_t clusters = items < held / c ? items : held / c;
-    d.ctas = whole ? clusters * c : kDecodeCtas * int64_t(device_sm_count());
+    d.mode = whole ? kClusters : kLine;
+    if (whole) d.cluster = static_cast<int>(c);
+    d.ctas = whole ? std::min(items, std::max<int64_t>(held / c, 1)) * c : kDecodeCtas * int64_t(device_sm_count());
     return d;
 }
 
-template <int D, int MT, bool ITEMS>
+template <int D, int MT, DecodeMode MODE>
 int launch_decode_as(const sa_kv_cache& cache, const PassParams& p, const DecodePlan& plan, cudaStream_t st)
 {
     using C = DecodeCfg<D, MT>;
-    auto kern = decode_kernel<D, MT, ITEMS>;
+    auto kern = decode_kernel<D, MT, MODE>;
     static bool attr_set[kMaxDevices] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SA_ERR_CUDA;
@@ -392,10 +403,11 @@ template <int D>
 int launch_decode(const sa_kv_cache& cache, const PassParams& p, const DecodePlan& plan, cudaStream_t st)
 {
     if (plan.mt == 1)
-        return plan.cluster ? launch_decode_as<D, 1, true>(cache, p, plan, st)
-                            : launch_decode_as<D, 1, false>(cache, p, plan, st);
-    return plan.cluster ? launch_decode_as<D, 2, true>(cache, p, plan, st)
-                        : launch_decode_as<D, 2, false>(cache, p, plan, st);
+        return plan.mode == kWarps      ? launch_decode_as<D, 1, kWarps>(cache, p, plan, st)
+               : plan.mode == kClusters ? launch_decode_as<D, 1, kClusters>(cache, p, plan, st)
+                                        : launch_decode_as<D, 1, kLine>(cache, p, plan, st);
+    return plan.mode == kClusters ? launch_decode_as<D, 2, kClusters>(cache, p, plan, st)
+                                  : launch_decode_as<D, 2, kLine>(cache, p, plan, st);
 }
 
 template <int D>
@@ -485,14 +497,16 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
     const int64_t most_q = most_new(p, max_q);
     const int64_t rows = most_q * p.group, all_rows = int64_t(p.T) * p.group;
     const int64_t held = kDecodeCtas * int64_t(device_sm_count());
-    const DecodePlan over = plan_decode<D>(p.prefix_len, 1, all_rows, p.Hkv, held);
+    const DecodePlan over = plan_decode<D>(p.prefix_len, 1, all_rows, p.Hkv, held, false);
     // whole items of the sequences run beside those of the prefix, for whose rows they wait at their ends
-    const int64_t beside = prefix && all_rows <= kDecodeRows && over.cluster > 0 ? std::max<int64_t>(held - over.ctas, 1) : held;
-    const DecodePlan plan = plan_decode<D>(most_keys(room, most_q), p.B, rows, p.Hkv, beside);
+    const bool whole_over = prefix && all_rows <= kDecodeRows && over.mode == kClusters;
+    const int64_t beside = whole_over ? std::max<int64_t>(held - over.ctas, 1) : held;
+    // the warps' line has more and smaller units: it is counted in 31 bits too
+    const bool by_warps = (all_rows / 16 + p.B) * p.Hkv <= INT_MAX / (room / DecodeCfg<D, 1>::TK + 8);
+    const DecodePlan plan = plan_decode<D>(most_keys(room, most_q), p.B, rows, p.Hkv, beside, by_warps);
     // Nothing is left for join_kernel where each item is finished by its CTAs; over a prefix the sequences'
     // pass then adds what the prefix's left.
-    const bool finished = rows <= kDecodeRows && plan.cluster > 0 &&
-                          (!prefix || (all_rows <= kDecodeRows && over.cluster > 0));
+    const bool finished = rows <= kDecodeRows && plan.mode == kClusters && (!prefix || whole_over);
     if (prefix) {
         // the rows of all sequences against the prefix
         PassParams pp = p;
@@ -549,7 +563,7 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
     if (p.B > 1) {
         PassParams pp = p;
         pp.rows_upto = p.group <= 16 ? 16 : kDecodeRows;
-        const DecodePlan line{pp.rows_upto <= 16 ? 1 : 2, 0, kDecodeCtas * int64_t(device_sm_count())};
+        const DecodePlan line{pp.rows_upto <= 16 ? 1 : 2, kLine, 1, kDecodeCtas * int64_t(device_sm_count())};
         use_tails(pp, 0, line.ctas, 16 * line.mt);
         if (int rc = launch_decode<D>(cache, pp, line, st)) return rc;
         p.rows_above = pp.rows_upto;

@@ -74,11 +74,6 @@ struct ChunkCfg {
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
 // 2^x for two lanes on the FMA pipe, as exp2_poly_x2 but of degree 5 (relative error
 // 2.2e-7, fitted by csrc/fit_exp2.py): the sum, which the LSE is taken from, then keeps
 // 32 bits' worth.  With degree 3 the LSE of rows with few keys was off by 7e-5; the two

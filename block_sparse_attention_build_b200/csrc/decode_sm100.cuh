@@ -16,10 +16,12 @@
 // from registers; a 128-row tcgen05 tile would be 7/8 padding and would pay the
 // trip through tensor memory for every tile of 16 keys.
 //
-// ITEMS = false: the line of units is cut evenly (see paged_sm100.cuh), cut items
-// are joined by join_kernel.  ITEMS = true, for items of few units: a cluster of
-// CTAs takes whole items, its CTAs every n-th unit of one, and the parts are added
-// over distributed shared memory, so that nothing has to follow.
+// kLine: the line of units is cut evenly (see paged_sm100.cuh), cut items are joined
+// by join_kernel.  kClusters, for items of few units: a cluster of CTAs takes whole
+// items, its CTAs every n-th unit of one, and the parts are added over distributed
+// shared memory, so that nothing has to follow.  kWarps, for many short items: the line
+// is cut evenly over the warps, which never meet, so that an item's end costs no
+// barrier and no idle warps.
 //
 // Code that runs once in a launch costs about 9 cycles an instruction (it comes
 // from L2: measured on the first and second pass over the same tile, 8660 and 1580
@@ -108,20 +110,26 @@ struct DecodeCfg {
     static constexpr int kTileBytes = TK * D * 2;
     static constexpr int kPanel = TK * 128;     // 64 columns x TK rows
     static constexpr int kOffMerge = kWarps * kStages * 2 * kTileBytes;
-    static constexpr int kOffMl = kOffMerge + 2 * R * D * 4;     // two warps' O
+    static constexpr int kOffQ = kOffMerge + 2 * R * D * 4;      // two warps' O
+    static constexpr int kOffMl = kOffQ + (MT == 2 ? R * D * 2 : 0);
     static constexpr int kOffRec = kOffMl + 2 * kWarps * R * 4;  // the warps' maxima and sums
     static constexpr int kOffBar = kOffRec + kWarps * kStages * static_cast<int>(sizeof(TileRec));
     static constexpr int kSmemBytes = kOffBar + kWarps * kStages * 8;
     static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
-template <int D, int MT, bool ITEMS>
+enum DecodeMode { kLine, kClusters, kWarps };
+
+template <int D, int MT, int MODE>
 __global__ void __launch_bounds__(128, 2)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ PassParams p)
 {
     using C = DecodeCfg<D, MT>;
-    constexpr int R = C::R, TK = C::TK, UK = C::UK, ST = C::kStages, NW = C::kWarps;
+    constexpr bool ITEMS = MODE == kClusters, WARP = MODE == kWarps;
+    constexpr int R = C::R, TK = C::TK, ST = C::kStages, NW = C::kWarps;
+    constexpr int UK = WARP ? TK : C::UK;  // keys of a unit: a tile of each warp, or one tile
+    static_assert(!WARP || MT == 1, "warps that never meet hold their queries in registers");
     constexpr int NF = D / 32;  // mma column tiles of a warp's quarter of the columns
     extern __shared__ __align__(1024) uint8_t smem[];  // swizzled tiles sit on 1024 bytes
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -129,6 +137,7 @@ __global__ void __launch_bounds__(128, 2)
     float4* merge = reinterpret_cast<float4*>(smem + C::kOffMerge);  // [2][MT][D / 8][32 lanes]
     float* sm_m = reinterpret_cast<float*>(smem + C::kOffMl);        // [NW][R]
     float* sm_l = sm_m + NW * R;
+    const uint32_t sq = smem_addr(smem + C::kOffQ);                  // MT = 2: the item's queries [R][D]
     TileRec* recs = reinterpret_cast<TileRec*>(smem + C::kOffRec) + warp * ST;
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * ST;
 
@@ -144,11 +153,12 @@ __global__ void __launch_bounds__(128, 2)
     launch_dependents();
     const SeqView ahead = peek_seq(p);
     // no tail rows yet (a segment's end, where there may be some, lies behind barriers)
-    if (!ITEMS && p.tails != nullptr && tid < R) p.tails[blockIdx.x * R + tid] = TailRow{0, 0};
-    const int rank = ITEMS ? static_cast<int>(cluster_rank()) : 0;
-    const int CL = ITEMS ? static_cast<int>(cluster_size()) : 1;
+    if (MODE == kLine && p.tails != nullptr && tid < R) p.tails[blockIdx.x * R + tid] = TailRow{0, 0};
+    const int rank = MODE == kClusters ? static_cast<int>(cluster_rank()) : 0;
+    const int CL = MODE == kClusters ? static_cast<int>(cluster_size()) : 1;
+    const int taker = WARP ? blockIdx.x * NW + warp : blockIdx.x;  // of a piece of the line
     const Piece piece = ITEMS ? find_piece<R, UK, true>(p, ahead, blockIdx.x / CL, gridDim.x / CL, 0)
-                              : find_piece<R, UK, false>(p, ahead, blockIdx.x, gridDim.x, 2);
+                              : find_piece<R, UK, false>(p, ahead, taker, WARP ? gridDim.x * NW : gridDim.x, 2);
     const int n_seq = p.over_prefix ? 1 : p.B;
 
     // ---- loads: this warp's tile of every unit of the piece, ST tiles ahead
@@ -170,7 +180,7 @@ __global__ void __launch_bounds__(128, 2)
     auto look_up_next = [&]() {
         nx.any = ITEMS ? left > 0 : pc.i < left;
         if (!nx.any) return;
-        const int k0 = pc.u.key(pc.i, UK) + warp * TK;
+        const int k0 = pc.u.key(pc.i, UK) + (WARP ? 0 : warp * TK);
         // boxes that begin below the item's last key; a tile with none completes its phase at once
         nx.nb = min((pc.u.hi - k0 + page_rows - 1) >> row_shift, TK >> row_shift);
         if (nx.nb < 0 || pc.i >= pc.u.nt) nx.nb = 0;  // ITEMS: a CTA may have no unit of an item
@@ -182,7 +192,7 @@ __global__ void __launch_bounds__(128, 2)
         const bool begins = ITEMS || u_item >= piece.u0, whole = ITEMS || (begins && pc.u.nt <= left);
         int parts = 0;
         if (!ITEMS && last && begins && !whole)
-            parts = cta_of(piece, u_item + pc.u.nt - 1) - static_cast<int>(blockIdx.x) + 1;
+            parts = cta_of(piece, u_item + pc.u.nt - 1) - taker + 1;
         nx.rec = TileRec{nx.nb > 0 ? k0 : INT32_MAX, (last ? 1 : 0) | (begins ? 2 : 0) | (whole ? 4 : 0) | rows << 3,
                          parts, pc.u.hi, pc.s.first, pc.rb, pc.h, p.prefix_len + pc.s.p0};
         if (ITEMS && last) left--;
@@ -226,7 +236,7 @@ __global__ void __launch_bounds__(128, 2)
     // ---- the piece's tiles
     const int rq = lane / 4, cq = (lane % 4) * 2;  // this lane's row (and row + 8) and column pair in an mma tile
     const int off = p.over_prefix ? 0 : p.prefix_len;  // position of key 0
-    uint32_t qf[MT][D / 16][4];
+    uint32_t qf[D / 16][4];  // MT = 1: the item's queries
     float o[MT][D / 8][4];
     float m_ref[MT][2], l_sum[MT][2];
     int row_lo[MT][2], row_hi[MT][2];  // keys this lane's rows see: row_lo .. row_hi, and those below cols
@@ -239,6 +249,7 @@ __global__ void __launch_bounds__(128, 2)
 #pragma unroll 1
     for (int j = 0; j < issued; j++) {
         const int st = j % ST;
+        const bool first_tile = fresh;
         if (fresh) {
             fresh = false;
             it = recs[st];
@@ -255,7 +266,21 @@ __global__ void __launch_bounds__(128, 2)
             hi_hi = min(p_hi - off, it.hi - 1);
             // over the prefix the rows' own positions matter unless every row sees every key
             const bool look_up = p.over_prefix && !(p_lo >= p.prefix_len - 1 && p.window >= 0 && p_hi <= p.window);
-            // Q fragments of the item's rows, straight from memory
+            if constexpr (MT == 2) {
+                // 32 rows' fragments would take 64 registers, and what spilled was read for every tile (32 sequences
+                // of up to 16384 keys, 32 rows a head: 295 us so, 138 like this).  To shared memory, chunks of 16
+                // bytes swizzled; every warp is past the barriers of the item before.
+#pragma unroll 1
+                for (int c = tid; c < R * (D / 8); c += C::kThreads) {
+                    const int r = c / (D / 8), ch = c % (D / 8);
+                    const int rr = r0 + min(r, rows_left - 1);  // rows behind the item's last repeat it
+                    const int i = div_group(p, rr);
+                    const int hq = it.h * p.group + rr - i * p.group;
+                    cp_async_16(sq + r * D * 2 + ((ch ^ (r & 7)) * 16),
+                                p.q + (it.first + i) * p.q_token + hq * p.q_head + ch * 8);
+                }
+            }
+            // MT = 1: Q fragments of the item's rows, straight from memory
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
 #pragma unroll
@@ -266,13 +291,16 @@ __global__ void __launch_bounds__(128, 2)
                     const int pos = look_up ? token_position(p, it.first + i) : p.over_prefix ? p_lo : it.base + i;
                     row_lo[mt][x] = first_seen(pos);
                     row_hi[mt][x] = min(pos - off, it.hi - 1);
-                    const __nv_bfloat16* src = p.q + (it.first + i) * p.q_token + (it.h * p.group + g) * p.q_head + cq;
+                    if constexpr (MT == 1) {
+                        const int hq = it.h * p.group + g;
+                        const __nv_bfloat16* src = p.q + (it.first + i) * p.q_token + hq * p.q_head + cq;
+                        const uint32_t* pairs = reinterpret_cast<const uint32_t*>(src);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; kk++)
+                        for (int kk = 0; kk < D / 16; kk++)
 #pragma unroll
-                        for (int y = 0; y < 2; y++)
-                            qf[mt][kk][x + 2 * y] =
-                                r < rows_left ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + y * 8)) : 0u;
+                            for (int y = 0; y < 2; y++)
+                                qf[kk][x + 2 * y] = r < rows_left ? __ldg(pairs + kk * 8 + y * 4) : 0u;
+                    }
                     m_ref[mt][x] = -INFINITY;
                     l_sum[mt][x] = 0.f;
                 }
@@ -286,6 +314,10 @@ __global__ void __launch_bounds__(128, 2)
         // tiles up to ST ahead: the stage of the last one has just been read
 #pragma unroll 1
         while (issued < j + ST && nx.any) issue();
+        if (MT == 2 && first_tile) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();
+        }
         const int k0 = recs[st].k0, flags = recs[st].flags, parts = recs[st].parts;
         const bool last = flags & 1;
         if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar[st], (j / ST) & 1, p.timeout))) {
@@ -319,7 +351,20 @@ __global__ void __launch_bounds__(128, 2)
                     for (int e = 0; e < 4; e++) s[mt][nb][e] = 0.f;
             // S = Q K^T: a matrix of 8 keys x 8 elements per quarter of the warp's addresses
 #pragma unroll
-            for (int kk = 0; kk < D / 32; kk++)
+            for (int kk = 0; kk < D / 32; kk++) {
+                uint32_t a[MT][2][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                    for (int y = 0; y < 2; y++) {
+                        if constexpr (MT == 2) {
+                            const int r = mt * 16 + lane % 16, c = kk * 4 + y * 2 + lane / 16;
+                            ldsm_x4(sq + r * D * 2 + ((c ^ (r & 7)) * 16), a[mt][y]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; e++) a[mt][y][e] = qf[2 * kk + y][e];
+                        }
+                    }
 #pragma unroll
                 for (int nb = 0; nb < TK / 8; nb++) {
                     const int row = nb * 8 + lane % 8;
@@ -328,10 +373,11 @@ __global__ void __launch_bounds__(128, 2)
                     ldsm_x4(ks + (kk * 32 / 64) * C::kPanel + row * 128 + ((ch ^ (row & 7)) * 16), b);
 #pragma unroll
                     for (int mt = 0; mt < MT; mt++) {
-                        mma_16816(s[mt][nb], qf[mt][2 * kk], b[0], b[1]);
-                        mma_16816(s[mt][nb], qf[mt][2 * kk + 1], b[2], b[3]);
+                        mma_16816(s[mt][nb], a[mt][0], b[0], b[1]);
+                        mma_16816(s[mt][nb], a[mt][1], b[2], b[3]);
                     }
                 }
+            }
             if (!full) {
 #pragma unroll
                 for (int mt = 0; mt < MT; mt++)
@@ -413,75 +459,11 @@ __global__ void __launch_bounds__(128, 2)
         __syncwarp();  // the stage is read
         if (!last) continue;
 
-        // ---- the item's last tile here: add the four warps.  Each warp's O goes to shared memory, two warps
-        // at a time, and each warp sums a quarter of the columns, weighted by 2^(its maximum - the common one).
-#pragma unroll
-        for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-            for (int x = 0; x < 2; x++) {
-                l_sum[mt][x] += __shfl_xor_sync(0xffffffffu, l_sum[mt][x], 1);
-                l_sum[mt][x] += __shfl_xor_sync(0xffffffffu, l_sum[mt][x], 2);
-                if (lane % 4 == 0) {
-                    sm_m[warp * R + mt * 16 + rq + 8 * x] = m_ref[mt][x];
-                    sm_l[warp * R + mt * 16 + rq + 8 * x] = l_sum[mt][x];
-                }
-            }
-        float M[MT][2], L[MT][2], acc[MT][NF][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-            for (int i = 0; i < NF; i++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) acc[mt][i][e] = 0.f;
-#pragma unroll 1
-        for (int half = 0; half < 2; half++) {
-            if (warp / 2 == half) {
-#pragma unroll
-                for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-                    for (int i = 0; i < D / 8; i++)
-                        merge[(((warp & 1) * MT + mt) * (D / 8) + i) * 32 + lane] =
-                            make_float4(o[mt][i][0], o[mt][i][1], o[mt][i][2], o[mt][i][3]);
-            }
-            __syncthreads();
-            if (half == 0) {
-#pragma unroll
-                for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-                    for (int x = 0; x < 2; x++) {
-                        const int r = mt * 16 + rq + 8 * x;
-                        M[mt][x] = fmaxf(fmaxf(sm_m[r], sm_m[R + r]), fmaxf(sm_m[2 * R + r], sm_m[3 * R + r]));
-                        L[mt][x] = 0.f;
-                    }
-            }
-#pragma unroll 1
-            for (int w = 2 * half; w < 2 * half + 2; w++) {
-#pragma unroll
-                for (int mt = 0; mt < MT; mt++) {
-                    float f[2];
-#pragma unroll
-                    for (int x = 0; x < 2; x++) {
-                        const int r = w * R + mt * 16 + rq + 8 * x;
-                        f[x] = sm_m[r] == -INFINITY ? 0.f : ex2_approx(sm_m[r] - M[mt][x]);
-                        L[mt][x] += f[x] * sm_l[r];
-                    }
-#pragma unroll
-                    for (int i = 0; i < NF; i++) {
-                        const float4 v = merge[(((w & 1) * MT + mt) * (D / 8) + warp * NF + i) * 32 + lane];
-                        acc[mt][i][0] += f[0] * v.x;
-                        acc[mt][i][1] += f[0] * v.y;
-                        acc[mt][i][2] += f[1] * v.z;
-                        acc[mt][i][3] += f[1] * v.w;
-                    }
-                }
-            }
-            __syncthreads();
-        }
+        // ---- the item's last tile here
         fresh = true;
-
         // An item that is not all in this piece leaves a part.
         const bool begins = flags & 2, whole = flags & 4;
-        const int slot = (2 * static_cast<int>(blockIdx.x) + (begins ? 1 : 0)) * R;
+        const int slot = (2 * taker + (begins ? 1 : 0)) * R;
         RowInfo ri{0, 0, 0, 0};
         if (!whole && begins)
             ri = RowInfo{p.part_row0 + slot, p.part_row0 + slot + R, parts, 2 * R};
@@ -520,87 +502,168 @@ __global__ void __launch_bounds__(128, 2)
                 for (int i = 0; i < N; i++) *reinterpret_cast<float2*>(dst + i * 8) = make_float2(v[i][0], v[i][1]);
                 if (first) (whole ? p.acc_ml[at] : p.part_ml[slot + r]) = make_float2(m, l);
             }
-            if (!ITEMS && first && p.tails != nullptr && begins && !whole)
+            if (MODE == kLine && first && p.tails != nullptr && begins && !whole)
                 p.tails[blockIdx.x * R + r] = TailRow{static_cast<int32_t>(at), ri.n};
             if (first && p.info != nullptr && begins)
                 p.info[at] = RowInfo{ri.first + (whole ? 0 : r), ri.second + (whole ? 0 : r), ri.n, ri.stride};
         };
-        if (ITEMS && CL > 1) {
-            // ---- add the CTAs of the cluster.  Of the item's F column pairs of two rows (in the order of the mma
-            // tiles' lanes) CTA k takes those from k F / CL on: all send theirs to its shared memory, with the
-            // rows' maxima and sums, and after one barrier it adds what came.
-            constexpr int F = MT * (D / 8) * 32;
-            const int shift = 31 - __clz(F) + 1 - __ffs(CL), share = 1 << shift;  // F / CL: both are powers of two
-            float2* got_ml = reinterpret_cast<float2*>(merge + F);  // [CL][R]
-            cluster_arrive();
-            cluster_wait();  // every CTA has added its warps: their buffer is free for what comes
+        if constexpr (WARP) {
 #pragma unroll
-            for (int mt = 0; mt < MT; mt++) {
+            for (int x = 0; x < 2; x++) {
+                float l = l_sum[0][x];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                float v[D / 8][2];
 #pragma unroll
-                for (int i = 0; i < NF; i++) {
-                    const int f = (mt * (D / 8) + warp * NF + i) * 32 + lane;
-                    cluster_st4(smem_addr(merge + rank * share + (f & (share - 1))), f >> shift,
-                                make_float4(acc[mt][i][0], acc[mt][i][1], acc[mt][i][2], acc[mt][i][3]));
+                for (int i = 0; i < D / 8; i++) {
+                    v[i][0] = o[0][i][2 * x];
+                    v[i][1] = o[0][i][2 * x + 1];
                 }
-#pragma unroll
-                for (int x = 0; x < 2; x++)  // lane 4 rq + c of warp w: to CTA w + 4 (c & 1)
-                    if (warp + 4 * (lane & 1) < CL && (lane & 3) < 2)
-                        cluster_st2(smem_addr(got_ml + rank * R + mt * 16 + rq + 8 * x), warp + 4 * (lane & 1),
-                                    make_float2(M[mt][x], L[mt][x]));
+                if (rq + 8 * x < rows_left)
+                    write(std::integral_constant<int, D / 8>{}, rq + 8 * x, cq, v, m_ref[0][x], l, lane % 4 == 0);
             }
-            __syncwarp();
-            cluster_arrive();
-            cluster_wait();
-            if (p.pre_acc != nullptr) wait_previous_kernel();
-#pragma unroll 1
-            for (int f0 = tid; f0 < share; f0 += C::kThreads) {
-                const int f = rank * share + f0;
-                const int r = f / ((D / 8) * 32) * 16 + f % 32 / 4, col = f / 32 % (D / 8) * 8 + f % 4 * 2;
-                float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, v[2][1][2] = {{{0.f, 0.f}}, {{0.f, 0.f}}};
-#pragma unroll 4
-                for (int k = 0; k < CL; k++)
-#pragma unroll
-                    for (int x = 0; x < 2; x++) m[x] = fmaxf(m[x], got_ml[k * R + r + 8 * x].x);
-#pragma unroll 4
-                for (int k = 0; k < CL; k++) {
-                    const float4 a = merge[k * share + f0];
-                    const float2 m0 = got_ml[k * R + r], m1 = got_ml[k * R + r + 8];
-                    const float w0 = m0.x == -INFINITY ? 0.f : ex2_approx(m0.x - m[0]);
-                    const float w1 = m1.x == -INFINITY ? 0.f : ex2_approx(m1.x - m[1]);
-                    v[0][0][0] += w0 * a.x;
-                    v[0][0][1] += w0 * a.y;
-                    v[1][0][0] += w1 * a.z;
-                    v[1][0][1] += w1 * a.w;
-                    l[0] += w0 * m0.y;
-                    l[1] += w1 * m1.y;
-                }
-#pragma unroll 1
-                for (int x = 0; x < 2; x++) {
-                    const bool hi = x;
-                    float u[1][2] = {{hi ? v[1][0][0] : v[0][0][0], hi ? v[1][0][1] : v[0][0][1]}};
-                    if (r + 8 * x < rows_left)
-                        write(std::integral_constant<int, 1>{}, r + 8 * x, col, u, hi ? m[1] : m[0], hi ? l[1] : l[0],
-                              col == 0);
-                }
-            }
-            if (j + 1 < issued) __syncthreads();  // read, before the next item's warps write there
         } else {
-            if (p.pre_acc != nullptr) wait_previous_kernel();
+            // ---- add the four warps.  Each warp's O goes to shared memory, two warps
+            // at a time, and each warp sums a quarter of the columns, weighted by 2^(its maximum - the common one).
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
 #pragma unroll
                 for (int x = 0; x < 2; x++) {
-                    const int r = mt * 16 + rq + 8 * x;
-                    if (r >= rows_left) continue;
-                    float v[NF][2];
+                    l_sum[mt][x] += __shfl_xor_sync(0xffffffffu, l_sum[mt][x], 1);
+                    l_sum[mt][x] += __shfl_xor_sync(0xffffffffu, l_sum[mt][x], 2);
+                    if (lane % 4 == 0) {
+                        sm_m[warp * R + mt * 16 + rq + 8 * x] = m_ref[mt][x];
+                        sm_l[warp * R + mt * 16 + rq + 8 * x] = l_sum[mt][x];
+                    }
+                }
+            float M[MT][2], L[MT][2], acc[MT][NF][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                for (int i = 0; i < NF; i++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) acc[mt][i][e] = 0.f;
+#pragma unroll 1
+            for (int half = 0; half < 2; half++) {
+                if (warp / 2 == half) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                        for (int i = 0; i < D / 8; i++)
+                            merge[(((warp & 1) * MT + mt) * (D / 8) + i) * 32 + lane] =
+                                make_float4(o[mt][i][0], o[mt][i][1], o[mt][i][2], o[mt][i][3]);
+                }
+                __syncthreads();
+                if (half == 0) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                        for (int x = 0; x < 2; x++) {
+                            const int r = mt * 16 + rq + 8 * x;
+                            M[mt][x] = fmaxf(fmaxf(sm_m[r], sm_m[R + r]), fmaxf(sm_m[2 * R + r], sm_m[3 * R + r]));
+                            L[mt][x] = 0.f;
+                        }
+                }
+#pragma unroll 1
+                for (int w = 2 * half; w < 2 * half + 2; w++) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++) {
+                        float f[2];
+#pragma unroll
+                        for (int x = 0; x < 2; x++) {
+                            const int r = w * R + mt * 16 + rq + 8 * x;
+                            f[x] = sm_m[r] == -INFINITY ? 0.f : ex2_approx(sm_m[r] - M[mt][x]);
+                            L[mt][x] += f[x] * sm_l[r];
+                        }
+#pragma unroll
+                        for (int i = 0; i < NF; i++) {
+                            const float4 v = merge[(((w & 1) * MT + mt) * (D / 8) + warp * NF + i) * 32 + lane];
+                            acc[mt][i][0] += f[0] * v.x;
+                            acc[mt][i][1] += f[0] * v.y;
+                            acc[mt][i][2] += f[1] * v.z;
+                            acc[mt][i][3] += f[1] * v.w;
+                        }
+                    }
+                }
+                __syncthreads();
+            }
+            if (MODE == kClusters && CL > 1) {
+                // ---- add the CTAs of the cluster.  Of the item's F column pairs of two rows (in the order of the mma
+                // tiles' lanes) CTA k takes those from k F / CL on: all send theirs to its shared memory, with the
+                // rows' maxima and sums, and after one barrier it adds what came.
+                constexpr int F = MT * (D / 8) * 32;
+                const int shift = 31 - __clz(F) + 1 - __ffs(CL), share = 1 << shift;  // F / CL: both are powers of two
+                float2* got_ml = reinterpret_cast<float2*>(merge + F);  // [CL][R]
+                cluster_arrive();
+                cluster_wait();  // every CTA has added its warps: their buffer is free for what comes
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++) {
 #pragma unroll
                     for (int i = 0; i < NF; i++) {
-                        v[i][0] = acc[mt][i][2 * x];
-                        v[i][1] = acc[mt][i][2 * x + 1];
+                        const int f = (mt * (D / 8) + warp * NF + i) * 32 + lane;
+                        cluster_st4(smem_addr(merge + rank * share + (f & (share - 1))), f >> shift,
+                                    make_float4(acc[mt][i][0], acc[mt][i][1], acc[mt][i][2], acc[mt][i][3]));
                     }
-                    write(std::integral_constant<int, NF>{}, r, warp * (D / 4) + cq, v, M[mt][x], L[mt][x],
-                          warp == 0 && lane % 4 == 0);
+#pragma unroll
+                    for (int x = 0; x < 2; x++)  // lane 4 rq + c of warp w: to CTA w + 4 (c & 1)
+                        if (warp + 4 * (lane & 1) < CL && (lane & 3) < 2)
+                            cluster_st2(smem_addr(got_ml + rank * R + mt * 16 + rq + 8 * x), warp + 4 * (lane & 1),
+                                        make_float2(M[mt][x], L[mt][x]));
                 }
+                __syncwarp();
+                cluster_arrive();
+                cluster_wait();
+                if (p.pre_acc != nullptr) wait_previous_kernel();
+#pragma unroll 1
+                for (int f0 = tid; f0 < share; f0 += C::kThreads) {
+                    const int f = rank * share + f0;
+                    const int r = f / ((D / 8) * 32) * 16 + f % 32 / 4, col = f / 32 % (D / 8) * 8 + f % 4 * 2;
+                    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, v[2][1][2] = {{{0.f, 0.f}}, {{0.f, 0.f}}};
+#pragma unroll 4
+                    for (int k = 0; k < CL; k++)
+#pragma unroll
+                        for (int x = 0; x < 2; x++) m[x] = fmaxf(m[x], got_ml[k * R + r + 8 * x].x);
+#pragma unroll 4
+                    for (int k = 0; k < CL; k++) {
+                        const float4 a = merge[k * share + f0];
+                        const float2 m0 = got_ml[k * R + r], m1 = got_ml[k * R + r + 8];
+                        const float w0 = m0.x == -INFINITY ? 0.f : ex2_approx(m0.x - m[0]);
+                        const float w1 = m1.x == -INFINITY ? 0.f : ex2_approx(m1.x - m[1]);
+                        v[0][0][0] += w0 * a.x;
+                        v[0][0][1] += w0 * a.y;
+                        v[1][0][0] += w1 * a.z;
+                        v[1][0][1] += w1 * a.w;
+                        l[0] += w0 * m0.y;
+                        l[1] += w1 * m1.y;
+                    }
+#pragma unroll 1
+                    for (int x = 0; x < 2; x++) {
+                        const bool hi = x;
+                        float u[1][2] = {{hi ? v[1][0][0] : v[0][0][0], hi ? v[1][0][1] : v[0][0][1]}};
+                        if (r + 8 * x < rows_left)
+                            write(std::integral_constant<int, 1>{}, r + 8 * x, col, u, hi ? m[1] : m[0],
+                                  hi ? l[1] : l[0], col == 0);
+                    }
+                }
+                if (j + 1 < issued) __syncthreads();  // read, before the next item's warps write there
+            } else {
+                if (p.pre_acc != nullptr) wait_previous_kernel();
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        const int r = mt * 16 + rq + 8 * x;
+                        if (r >= rows_left) continue;
+                        float v[NF][2];
+#pragma unroll
+                        for (int i = 0; i < NF; i++) {
+                            v[i][0] = acc[mt][i][2 * x];
+                            v[i][1] = acc[mt][i][2 * x + 1];
+                        }
+                        write(std::integral_constant<int, NF>{}, r, warp * (D / 4) + cq, v, M[mt][x], L[mt][x],
+                              warp == 0 && lane % 4 == 0);
+                    }
+            }
         }
     }
     if (dead) {

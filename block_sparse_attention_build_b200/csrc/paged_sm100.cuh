@@ -394,6 +394,11 @@ __device__ __forceinline__ int page_of(const PassParams& p, int entry)
     return entry >= 0 && entry < p.n_pages ? entry : p.n_pages;
 }
 
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 __device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3,
                                             int c4)
 {

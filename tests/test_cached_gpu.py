@@ -207,6 +207,71 @@ def test_more_items_than_clusters():
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("prefix", [0, 500])
+@pytest.mark.parametrize("q_len,Hq,Hkv,kv_max", [(1, 8, 4, 600), (1, 16, 8, 30), (4, 8, 2, 300), (2, 40, 5, 900),
+                                                 (1, 7, 7, 17)])
+def test_short_sequences_cut_over_the_warps(q_len, Hq, Hkv, kv_max, prefix, D):
+    """An item or more to every CTA and few keys to each; empty sequences and lengths of one among them."""
+    B = -(-600 // Hkv) + 37
+    m = [q_len if b % 11 else b % 2 for b in range(B)]
+    kv = [max(n, 1 + (53 * b) % kv_max) if b % 13 else n for b, n in enumerate(m)]
+    go(Case(m, kv, Hq=Hq, Hkv=Hkv, D=D, page=16, prefix=prefix, seed=111), ALL)
+    go(Case(m, kv, Hq=Hq, Hkv=Hkv, D=D, page=64, prefix=prefix, seed=112), sa.Pattern(window=kv_max // 2, sinks=3))
+    go(Case(m, kv, Hq=Hq, Hkv=Hkv, D=D, page=32, prefix=prefix, seed=113), sa.Pattern(window=-1, sinks=5))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("prefix", [0, 300])
+@pytest.mark.parametrize("q_len,Hq,Hkv", [(8, 8, 2), (5, 5, 1), (1, 17, 1), (1, 62, 2), (17, 3, 3)])
+def test_seventeen_to_thirty_two_rows(q_len, Hq, Hkv, prefix, D):
+    for B, far in ((3, 700), (30, 5000)):
+        kv = [q_len + (31 + far * b // 7) % far for b in range(B)]
+        m = [q_len - b % 2 for b in range(B)]
+        go(Case(m, kv, Hq=Hq, Hkv=Hkv, D=D, prefix=prefix, seed=121), ALL)
+        go(Case(m, kv, Hq=Hq, Hkv=Hkv, D=D, prefix=prefix, seed=122), sa.Pattern(window=200, sinks=40))
+
+
+def test_a_warp_whose_wait_runs_out():
+    """As test_a_wait_that_runs_out, where the warps of a CTA work on pieces of their own."""
+    c = Case([1] * 160, [1 + (53 * b) % 200 for b in range(160)], Hq=8, Hkv=4, seed=166)
+    args = (c.dev(c.q), c.cache(), c.batch(1))
+    try:
+        sa.set_debug(sa.DEBUG_SKIP_Q_LOAD, 20_000_000)
+        sa.fwd_cached(*args, ALL)
+        assert sa.check_device() == sa.SA_ERR_DEVICE_TIMEOUT
+    finally:
+        sa.set_debug(0, 0)
+    assert sa.check_device() == sa.SA_OK
+    c.check(*sa.fwd_cached(*args, ALL), ALL)
+
+
+def test_short_sequences_of_graphs_sharing_a_workspace():
+    """Two captured steps over one workspace, replayed in turn with other lengths of their sequences."""
+    c = Case([1] * 160, [1 + (53 * b) % 400 for b in range(160)], Hq=8, Hkv=4, page=16, seed=167)
+    d = Case([2] * 160, [2 + (91 * b) % 300 for b in range(160)], Hq=8, Hkv=4, page=16, seed=168)
+    ws = torch.empty(max(sa.fwd_cached_workspace_bytes(x.T, x.Hq, x.Hkv, x.D) for x in (c, d)), dtype=torch.uint8,
+                     device="cuda")
+    steps = []
+    for x in (c, d):
+        args = (x.dev(x.q), x.cache(), x.batch(max(x.q_len)))
+        sa.fwd_cached(*args, ALL, workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = sa.fwd_cached(*args, ALL, workspace=ws)
+        steps.append((x, g, args, out))
+    for _ in range(3):
+        for x, g, args, out in steps:
+            g.replay()
+            x.check(*out, ALL)
+    for x, g, args, out in steps:
+        x.kv_len = [n - (3 if n > 9 else 0) for n in x.kv_len]
+        x.k, x.v = ([y[:n] for y, n in zip(z, x.kv_len)] for z in (x.k, x.v))
+        args[2].kv_len.copy_(torch.tensor(x.kv_len, dtype=torch.int32))
+        g.replay()
+        x.check(*out, ALL)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("q_len", [1, 3, 70, 300])
 @pytest.mark.parametrize("prefix", [0, 500])
 def test_infinities_in_places_no_row_sees(q_len, prefix, D):
