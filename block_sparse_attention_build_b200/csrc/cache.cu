@@ -505,8 +505,18 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
     const bool by_warps = (all_rows / 16 + p.B) * p.Hkv <= INT_MAX / (room / DecodeCfg<D, 1>::TK + 8);
     const DecodePlan plan = plan_decode<D>(most_keys(room, most_q), p.B, rows, p.Hkv, beside, by_warps);
     // Nothing is left for join_kernel where each item is finished by its CTAs; over a prefix the sequences'
-    // pass then adds what the prefix's left.
-    const bool finished = rows <= kDecodeRows && plan.mode == kClusters && (!prefix || whole_over);
+    // pass then adds what the prefix's left: whole rows, or the parts of cut ones where these are few (122 rows a
+    // head behind 151 tokens, 2 parts: 25.2 us with join_kernel, 21.4 without; 12 sequences behind 1223, 15 parts:
+    // 23.0 and 21.4; behind 12230, 20 parts: 31.2 and 34.1).
+    auto parts_over = [&]() {
+        const bool few = all_rows <= kDecodeRows;
+        const int64_t R = few ? 16 * over.mt : ChunkCfg<D>::R, ctas = few ? over.ctas : device_sm_count();
+        const int64_t UK = few ? DecodeCfg<D, 1>::UK : ChunkCfg<D>::UK;
+        const int64_t units = most_keys(p.prefix_len, most_q) / UK + 3;
+        return std::min(units, ctas / ((all_rows + R - 1) / R * p.Hkv) + 2);
+    };
+    const bool finished = rows <= kDecodeRows && plan.mode == kClusters &&
+                          (!prefix || whole_over || parts_over() <= 16);
     if (prefix) {
         // the rows of all sequences against the prefix
         PassParams pp = p;
@@ -514,7 +524,7 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
         pp.table = prefix_table;
         pp.table_stride = 0;
         use_parts(pp, w, ws, 1, w.rows_decode + w.rows_chunk, D, true);
-        if (finished) pp.info = nullptr;
+        if (finished && whole_over) pp.info = nullptr;
         if (int rc = all_rows <= kDecodeRows ? launch_decode<D>(cache, pp, over, st) : launch_chunk<D>(cache, pp, st))
             return rc;
         p.first_kernel = 0;
@@ -526,6 +536,12 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
         if (prefix) {
             p.pre_acc = reinterpret_cast<const float*>(ws + w.acc[1]);
             p.pre_ml = reinterpret_cast<const float2*>(ws + w.acc_ml[1]);
+            if (!whole_over) {
+                p.pre_info = j.info[1];
+                p.pre_part_o = j.part_o;
+                p.pre_part_ml = j.part_ml;
+                p.part_rows = j.part_rows;
+            }
         }
         return launch_decode<D>(cache, p, plan, st);
     }

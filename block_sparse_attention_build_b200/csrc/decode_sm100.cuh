@@ -476,19 +476,46 @@ __global__ void __launch_bounds__(128, 2)
             const int hq = it.h * p.group + rr - i_tok * p.group;
             const int64_t at = t * p.Hq + hq;
             if (whole && p.acc == nullptr) {
-                if (p.pre_acc != nullptr) {  // add the row's part over the prefix
-                    const float2 ml = p.pre_ml[at];
-                    const float mn = fmaxf(m, ml.x);
-                    const float fo = m == -INFINITY ? 0.f : ex2_approx(m - mn);
-                    const float fn = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
+                if (MODE == kClusters && p.pre_acc != nullptr) {  // add the row's part over the prefix, or its parts
+                    auto add = [&](const float2 (&w)[N], float2 ml) {
+                        const float mn = fmaxf(m, ml.x);
+                        const float fo = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+                        const float fn = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
 #pragma unroll
-                    for (int i = 0; i < N; i++) {
-                        const float2 w = *reinterpret_cast<const float2*>(p.pre_acc + at * D + col + i * 8);
-                        v[i][0] = v[i][0] * fo + w.x * fn;
-                        v[i][1] = v[i][1] * fo + w.y * fn;
+                        for (int i = 0; i < N; i++) {
+                            v[i][0] = v[i][0] * fo + w[i].x * fn;
+                            v[i][1] = v[i][1] * fo + w[i].y * fn;
+                        }
+                        l = l * fo + ml.y * fn;
+                        m = mn;
+                    };
+                    RowInfo pi{0, 0, 0, 0};
+                    if (p.pre_info != nullptr) pi = p.pre_info[at];
+                    if (pi.n == 0) {
+                        float2 w[N];
+#pragma unroll
+                        for (int i = 0; i < N; i++)
+                            w[i] = *reinterpret_cast<const float2*>(p.pre_acc + at * D + col + i * 8);
+                        add(w, p.pre_ml[at]);
+                    } else if (in_range(pi, p.part_rows)) {
+                        constexpr int K = N == 1 ? 4 : 2;  // in flight
+#pragma unroll 1
+                        for (int k0 = 0; k0 < pi.n; k0 += K) {
+                            float2 ml[K], w[K][N];
+#pragma unroll
+                            for (int k = 0; k < K; k++) {
+                                const int kk = min(k0 + k, pi.n - 1);  // past the last: not added
+                                const int64_t from = kk == 0 ? pi.first : pi.second + int64_t(kk - 1) * pi.stride;
+                                ml[k] = p.pre_part_ml[from];
+#pragma unroll
+                                for (int i = 0; i < N; i++)
+                                    w[k][i] = *reinterpret_cast<const float2*>(p.pre_part_o + from * D + col + i * 8);
+                            }
+#pragma unroll
+                            for (int k = 0; k < K; k++)
+                                if (k0 + k < pi.n) add(w[k], ml[k]);
+                        }
                     }
-                    l = l * fo + ml.y * fn;
-                    m = mn;
                 }
                 const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
                 __nv_bfloat16* dst = p.o + t * p.o_token + hq * p.o_head + col;
@@ -647,7 +674,7 @@ __global__ void __launch_bounds__(128, 2)
                 }
                 if (j + 1 < issued) __syncthreads();  // read, before the next item's warps write there
             } else {
-                if (p.pre_acc != nullptr) wait_previous_kernel();
+                if (MODE == kClusters && p.pre_acc != nullptr) wait_previous_kernel();
 #pragma unroll
                 for (int mt = 0; mt < MT; mt++)
 #pragma unroll

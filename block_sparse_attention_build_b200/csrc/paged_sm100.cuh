@@ -46,6 +46,14 @@ struct alignas(16) RowInfo {
     int32_t first, second, n, stride;
 };
 
+// A row that no sequence covers (q_start not ascending from 0) has no entry: nothing of one that is out of range
+// is followed.
+__device__ __forceinline__ bool in_range(const RowInfo& r, int part_rows)
+{
+    return r.n >= 0 && r.n <= part_rows && r.stride >= 0 && r.stride <= part_rows && r.first >= 0 && r.second >= 0 &&
+           (r.n == 0 || (r.first < part_rows && r.second + static_cast<int64_t>(r.n - 2) * r.stride < part_rows));
+}
+
 // The same from the other side, where rows are many and few of them are cut: the
 // rows of each CTA's tail slot (n = 0: none), R entries a CTA.
 struct alignas(8) TailRow {
@@ -80,6 +88,10 @@ struct PassParams {
     float2* acc_ml;            // [T, Hq]
     const float* pre_acc;      // not null: what the pass over the prefix left, added to every row
     const float2* pre_ml;
+    const RowInfo* pre_info;   // not null: rows of that pass may lie in parts instead, of the arrays
+    const float* pre_part_o;   // that join_kernel reads
+    const float2* pre_part_ml;
+    int32_t part_rows;
     int32_t first_kernel;      // 1: the call's first kernel (what came before on the stream is not the call's)
     int32_t* status;
     long long timeout;
@@ -529,13 +541,7 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p)
 #pragma unroll
             for (int s = 0; s < (PREFIX ? 2 : 1); s++) {
                 const RowInfo ri = p.info[s][row];
-                // a row that no sequence covers (q_start not ascending from 0) has no entry: nothing of it
-                // is followed
-                if (ri.n < 0 || ri.n > p.part_rows || ri.stride < 0 || ri.stride > p.part_rows || ri.first < 0 ||
-                    ri.second < 0 ||
-                    (ri.n > 0 && (ri.first >= p.part_rows ||
-                                  ri.second + static_cast<int64_t>(ri.n - 2) * ri.stride >= p.part_rows)))
-                    continue;
+                if (!in_range(ri, p.part_rows)) continue;
                 if (ri.n == 0) {
                     if (PREFIX && sub == 0) {
                         float v[E];

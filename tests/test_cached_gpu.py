@@ -439,3 +439,19 @@ def test_other_device_than_the_current_one():
     with torch.cuda.device(0):
         o, lse = sa.fwd_cached(c.dev(c.q), c.cache(), c.batch(40), WS)
     c.check(o, lse, WS)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_len,Hq,Hkv,B,prefix", [(1, 8, 2, 40, 700), (2, 32, 8, 30, 151), (1, 32, 8, 6, 1500),
+                                                   (3, 16, 2, 25, 1033), (1, 20, 1, 9, 90), (8, 8, 2, 2, 640)])
+def test_parts_of_a_prefix_added_by_the_sequences_pass(q_len, Hq, Hkv, B, prefix, D):
+    """Few keys of its own to each sequence, behind a prefix whose items are cut into a few parts."""
+    m = [q_len if b % 5 else b % 2 for b in range(B)]
+    m[0] = q_len
+    kv = [max(n, (37 * b) % 130) for b, n in enumerate(m)]
+    for page, pattern in ((32, ALL), (64, sa.Pattern(window=120, sinks=70)), (16, sa.Pattern(window=-1, sinks=300))):
+        c = Case(m, kv, Hq=Hq, Hkv=Hkv, D=D, page=page, prefix=prefix, pad_rows=3, seed=171)
+        o, lse = go(c, pattern)
+        again, l_again = c.run(pattern)
+        T = int(c.q_start[-1])
+        assert torch.equal(o[:T], again[:T]) and torch.equal(lse[:T], l_again[:T])
