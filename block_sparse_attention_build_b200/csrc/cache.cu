@@ -74,8 +74,8 @@ RotSpec rot_spec(const sa_rotary* r)
     return s;
 }
 
-// A launch that may be set up while the stream's previous kernel still runs; it waits
-// for it where it has to, a call's first kernel at once.  In clusters of `cluster`.
+// A launch that may be set up while the stream's previous kernel still runs; the kernel waits for that one
+// before its first access to memory.  In clusters of `cluster`.
 template <typename... Args>
 int launch_after(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster, const Args&... args)
 {
@@ -487,7 +487,6 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
     const bool prefix = p.prefix_len > 0;
     p.rows_above = 0;
     p.rows_upto = INT_MAX;
-    p.first_kernel = 1;
     // most keys of an item, out of `room`: what the window, the sinks and an item's tokens span
     auto most_keys = [&](int64_t room, int64_t tokens) {
         if (p.n_global > 0 || p.window < 0) return p.n_global > 0 ? room : std::min<int64_t>(room, p.cols);
@@ -498,12 +497,10 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
     const int64_t rows = most_q * p.group, all_rows = int64_t(p.T) * p.group;
     const int64_t held = kDecodeCtas * int64_t(device_sm_count());
     const DecodePlan over = plan_decode<D>(p.prefix_len, 1, all_rows, p.Hkv, held, false);
-    // whole items of the sequences run beside those of the prefix, for whose rows they wait at their ends
     const bool whole_over = prefix && all_rows <= kDecodeRows && over.mode == kClusters;
-    const int64_t beside = whole_over ? std::max<int64_t>(held - over.ctas, 1) : held;
     // the warps' line has more and smaller units: it is counted in 31 bits too
     const bool by_warps = (all_rows / 16 + p.B) * p.Hkv <= INT_MAX / (room / DecodeCfg<D, 1>::TK + 8);
-    const DecodePlan plan = plan_decode<D>(most_keys(room, most_q), p.B, rows, p.Hkv, beside, by_warps);
+    const DecodePlan plan = plan_decode<D>(most_keys(room, most_q), p.B, rows, p.Hkv, held, by_warps);
     // Nothing is left for join_kernel where each item is finished by its CTAs; over a prefix the sequences'
     // pass then adds what the prefix's left: whole rows, or the parts of cut ones where these are few (122 rows a
     // head behind 151 tokens, 2 parts: 25.2 us with join_kernel, 21.4 without; 12 sequences behind 1223, 15 parts:
@@ -527,7 +524,6 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
         if (finished && whole_over) pp.info = nullptr;
         if (int rc = all_rows <= kDecodeRows ? launch_decode<D>(cache, pp, over, st) : launch_chunk<D>(cache, pp, st))
             return rc;
-        p.first_kernel = 0;
     }
     // each sequence against its own tokens: by decode_kernel alone where no sequence is known to have
     // more than its rows (it can take any), by chunk_kernel alone where there is one sequence of many rows,
@@ -583,7 +579,6 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
         use_tails(pp, 0, line.ctas, 16 * line.mt);
         if (int rc = launch_decode<D>(cache, pp, line, st)) return rc;
         p.rows_above = pp.rows_upto;
-        p.first_kernel = 0;
     }
     use_parts(p, w, ws, 0, w.rows_decode, D, prefix);
     use_tails(p, 1, device_sm_count(), ChunkCfg<D>::R);

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(384, 1)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    if (p.first_kernel) wait_previous_kernel();
+    wait_previous_kernel();
     launch_dependents();
     if (p.tails != nullptr && threadIdx.x < R) p.tails[blockIdx.x * R + threadIdx.x] = TailRow{0, 0};
     Piece piece;
@@ -648,7 +648,6 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after_sync();
         tmem_dealloc(tmem, C::kTmemCols);
     }
-    wait_previous_kernel();
 }
 
 }  // namespace sa

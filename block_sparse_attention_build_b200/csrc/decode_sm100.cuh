@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(128, 2)
         tma_prefetch_desc(&tmV);
     }
     __syncwarp();
-    if (p.first_kernel) wait_previous_kernel();
+    wait_previous_kernel();
     launch_dependents();
     const SeqView ahead = peek_seq(p);
     // no tail rows yet (a segment's end, where there may be some, lies behind barriers)
@@ -228,10 +228,7 @@ __global__ void __launch_bounds__(128, 2)
         if (!dead) live = issued;
     };
     look_up_next();
-    if (!nx.any) {
-        wait_previous_kernel();
-        return;
-    }
+    if (!nx.any) return;
 
     // ---- the piece's tiles
     const int rq = lane / 4, cq = (lane % 4) * 2;  // this lane's row (and row + 8) and column pair in an mma tile
@@ -299,7 +296,7 @@ __global__ void __launch_bounds__(128, 2)
                         for (int kk = 0; kk < D / 16; kk++)
 #pragma unroll
                             for (int y = 0; y < 2; y++)
-                                qf[kk][x + 2 * y] = r < rows_left ? __ldg(pairs + kk * 8 + y * 4) : 0u;
+                                qf[kk][x + 2 * y] = r < rows_left ? pairs[kk * 8 + y * 4] : 0u;
                     }
                     m_ref[mt][x] = -INFINITY;
                     l_sum[mt][x] = 0.f;
@@ -640,7 +637,6 @@ __global__ void __launch_bounds__(128, 2)
                 __syncwarp();
                 cluster_arrive();
                 cluster_wait();
-                if (p.pre_acc != nullptr) wait_previous_kernel();
 #pragma unroll 1
                 for (int f0 = tid; f0 < share; f0 += C::kThreads) {
                     const int f = rank * share + f0;
@@ -674,7 +670,6 @@ __global__ void __launch_bounds__(128, 2)
                 }
                 if (j + 1 < issued) __syncthreads();  // read, before the next item's warps write there
             } else {
-                if (MODE == kClusters && p.pre_acc != nullptr) wait_previous_kernel();
 #pragma unroll
                 for (int mt = 0; mt < MT; mt++)
 #pragma unroll
@@ -697,7 +692,6 @@ __global__ void __launch_bounds__(128, 2)
         // copies still in flight land before the CTA's memory goes away
         for (int j = max(live - ST, 0); j < live; j++) mbar_wait(&bar[j % ST], (j / ST) & 1, p.timeout);
     }
-    wait_previous_kernel();
 }
 
 }  // namespace sa

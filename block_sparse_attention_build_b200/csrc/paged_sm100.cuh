@@ -60,6 +60,10 @@ struct alignas(8) TailRow {
     int32_t row, n;  // token * Hq + head; parts
 };
 
+// Every kernel is launched while the one before it on the stream may still run, and reads or writes memory only
+// behind griddepcontrol.wait: nothing else promises it the writes of the kernels before, not even of those that the
+// previous one has waited for.  All of what it reads may have been written after its launch, so its loads are plain
+// ones: the non-coherent path is for data that does not change while a kernel lives.
 struct PassParams {
     const __nv_bfloat16* q;
     int64_t q_token, q_head;
@@ -92,7 +96,6 @@ struct PassParams {
     const float* pre_part_o;   // that join_kernel reads
     const float2* pre_part_ml;
     int32_t part_rows;
-    int32_t first_kernel;      // 1: the call's first kernel (what came before on the stream is not the call's)
     int32_t* status;
     long long timeout;
     int32_t debug_flags;
@@ -111,7 +114,7 @@ struct SeqView {
 // Tokens of sequence b in the cache: no more than its table has room for.
 __device__ __forceinline__ int cached_len(const PassParams& p, int b)
 {
-    return min(max(__ldg(&p.kv_len[b]), 0), p.max_pages << p.page_shift);
+    return min(max(p.kv_len[b], 0), p.max_pages << p.page_shift);
 }
 
 __device__ __forceinline__ SeqView load_seq(const PassParams& p, int b)
@@ -119,13 +122,13 @@ __device__ __forceinline__ SeqView load_seq(const PassParams& p, int b)
     SeqView s;
     if (p.over_prefix) {
         s.first = 0;
-        s.m = min(max(__ldg(&p.q_start[p.B]), 0), p.T);
+        s.m = min(max(p.q_start[p.B], 0), p.T);
         s.len = p.prefix_len;
         s.p0 = 0;  // differs from row to row: see PassBounds
     } else {
-        const int a = min(max(__ldg(&p.q_start[b]), 0), p.T);
+        const int a = min(max(p.q_start[b], 0), p.T);
         s.first = a;
-        s.m = max(min(__ldg(&p.q_start[b + 1]), p.T) - a, 0);
+        s.m = max(min(p.q_start[b + 1], p.T) - a, 0);
         s.len = cached_len(p, b);
         s.p0 = s.len - s.m;
     }
@@ -194,12 +197,12 @@ __device__ __forceinline__ int token_position(const PassParams& p, int t)
     int lo = 0, hi = p.B;  // q_start[lo] <= t < q_start[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (__ldg(&p.q_start[mid]) <= t)
+        if (p.q_start[mid] <= t)
             lo = mid;
         else
             hi = mid;
     }
-    const int first = __ldg(&p.q_start[lo]), next = __ldg(&p.q_start[lo + 1]);
+    const int first = p.q_start[lo], next = p.q_start[lo + 1];
     return p.prefix_len + cached_len(p, lo) - (next - first) + (t - first);
 }
 
@@ -264,7 +267,7 @@ __device__ __forceinline__ PassBounds pass_bounds(const PassParams& p)
     int lo = INT32_MAX, hi = INT32_MIN;
 #pragma unroll 1
     for (int b = threadIdx.x % 32; b < p.B; b += 32) {
-        const int m = __ldg(&p.q_start[b + 1]) - __ldg(&p.q_start[b]);
+        const int m = p.q_start[b + 1] - p.q_start[b];
         const int last = p.prefix_len + cached_len(p, b) - 1;
         if (m <= 0) continue;
         lo = min(lo, last - m + 1);
@@ -399,7 +402,7 @@ __device__ __forceinline__ int cta_of(const Piece& r, int u)
 // before it is looked at.
 __device__ __forceinline__ int page_entry(const PassParams& p, int b, int k)
 {
-    return __ldg(&p.table[static_cast<int64_t>(b) * p.table_stride + (k >> p.page_shift)]);
+    return p.table[static_cast<int64_t>(b) * p.table_stride + (k >> p.page_shift)];
 }
 __device__ __forceinline__ int page_of(const PassParams& p, int entry)
 {
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p)
     const int sub = warp % WPR;
     __shared__ float sh_o[8][D];
     __shared__ float sh_m[8], sh_l[8];
-    const int64_t total = static_cast<int64_t>(min(max(__ldg(&p.q_start[p.B]), 0), p.T)) * p.Hq;
+    const int64_t total = static_cast<int64_t>(min(max(p.q_start[p.B], 0), p.T)) * p.Hq;
     // every warp of a block makes the same number of rounds
     for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < total;
          row0 += static_cast<int64_t>(gridDim.x) * kRows) {

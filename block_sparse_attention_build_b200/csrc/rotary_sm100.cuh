@@ -199,21 +199,21 @@ __global__ void __launch_bounds__(kRotThreads, rot_blocks(LAYOUT)) rotary_kernel
         const int mine = static_cast<int>(t - t0);
         int cnt = 0;
         for (int c = 0; c < p.B; c += 32) {
-            const int s = c + lane < p.B ? __ldg(&p.q_start[c + lane]) : INT32_MAX;
+            const int s = c + lane < p.B ? p.q_start[c + lane] : INT32_MAX;
 #pragma unroll
             for (int k = 0; k < kTok; k++) {
                 const int m = __popc(__ballot_sync(0xffffffffu, s <= t0 + k));
                 if (k == mine) cnt += m;
             }
         }
-        have = t < p.rows && cnt > 0 && t < __ldg(&p.q_start[p.B]);
+        have = t < p.rows && cnt > 0 && t < p.q_start[p.B];
         b = max(cnt - 1, 0);
-        const int first = __ldg(&p.q_start[b]), next = __ldg(&p.q_start[b + 1]);
+        const int first = p.q_start[b], next = p.q_start[b + 1];
         n = t;
-        place = __ldg(&p.kv_len[b]) - (next - first) + static_cast<int>(t - first);
+        place = p.kv_len[b] - (next - first) + static_cast<int>(t - first);
         const int pi = place >> p.page_shift;
         if (have && place >= 0 && pi < p.max_pages) {
-            const int page = __ldg(&p.table[b * p.table_stride + pi]);
+            const int page = p.table[b * p.table_stride + pi];
             if (page >= 0 && page < p.n_pages)
                 page_off = page * p.ko.batch + (place & ((1 << p.page_shift) - 1)) * p.ko.token;
         }
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kRotThreads, rot_blocks(LAYOUT)) rotary_kernel
             if (PAGED && p.pos == nullptr)
                 pos = place + p.pos_offset;
             else
-                pos = __ldg(&p.pos[sh_axis[j] * p.pos_axis + (PAGED ? t : b * p.pos_batch + n)]);
+                pos = p.pos[sh_axis[j] * p.pos_axis + (PAGED ? t : b * p.pos_batch + n)];
             // the angle modulo a turn: the low 64 bits of the product, of which the upper 32 are kept
             const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos)) * sh_turns[j];
             sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn[i], &cs[i]);
