@@ -74,6 +74,13 @@ struct ChunkCfg {
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // 2^x for two lanes on the FMA pipe, as exp2_poly_x2 but of degree 5 (relative error
 // 2.2e-7, fitted by csrc/fit_exp2.py): the sum, which the LSE is taken from, then keeps
 // 32 bits' worth.  With degree 3 the LSE of rows with few keys was off by 7e-5; the two
@@ -93,10 +100,12 @@ __device__ __forceinline__ void exp2_poly5_x2(uint64_t x2, float& p0, float& p1)
     float x0, x1, t0, t1, q0, q1;
     f2_unpack(x2, x0, x1);
     f2_unpack(t2, t0, t1);
-    f2_unpack(q2, q0, q1);
-    // the low bits of t hold j (two's complement); shifting them into the exponent field scales by 2^j
-    p0 = x0 < -125.f ? 0.f : __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
-    p1 = x1 < -125.f ? 0.f : __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
+    // the low bits of t hold j (two's complement): shifted into the exponent field of 1 they make 2^j, by which q
+    // is multiplied (added to q's own bits they would make 3.4e38 of a NaN)
+    f2_unpack(f2_mul(q2, f2_pack(__int_as_float(0x3f800000 + (__float_as_int(t0) << 23)),
+                                 __int_as_float(0x3f800000 + (__float_as_int(t1) << 23)))), q0, q1);
+    p0 = x0 < -125.f ? 0.f : q0;
+    p1 = x1 < -125.f ? 0.f : q1;
 }
 
 template <int D>
