@@ -456,6 +456,10 @@ struct TailJoinParams {
     int32_t part_rows;
 };
 
+// A part in which a row sees nothing.  A part whose scores are all NaN keeps its maximum of -inf too (the maximum
+// drops them), but its sum is NaN: it is added, and the row is NaN whichever part it comes from.
+__device__ __forceinline__ bool no_part(float2 ml) { return ml.x == -INFINITY && ml.y == 0.f; }
+
 // A row's parts added up by one warp, E elements a lane: O = sum of O_k 2^(m_k - M)
 // over L = sum of l_k 2^(m_k - M), M the largest m_k, in the order they come.
 template <int D>
@@ -472,7 +476,7 @@ struct RowSum {
     }
     __device__ __forceinline__ void add(const float (&v)[E], float2 ml)
     {
-        if (ml.x == -INFINITY) return;
+        if (no_part(ml)) return;
         const float mn = fmaxf(M, ml.x);
         const float a = ex2_approx(M - mn), b = ex2_approx(ml.x - mn);
 #pragma unroll
@@ -616,7 +620,7 @@ __global__ void __launch_bounds__(256) join_tails_kernel(const TailJoinParams p)
         }
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-            if (ml[j].x == -INFINITY) continue;
+            if (no_part(ml[j])) continue;
             const float mn = fmaxf(M, ml[j].x);
             const float a = ex2_approx(M - mn), b = ex2_approx(ml[j].x - mn);
 #pragma unroll

@@ -89,7 +89,7 @@ def check(c, clean, pattern):
 
 
 @pytest.mark.parametrize("pattern", [ALL, WS], ids=["all", "w100s4"])
-@pytest.mark.parametrize("what", ["key 16", "key 17"])
+@pytest.mark.parametrize("what", ["query", "query inf", "page", "key 16", "key 17", "prefix page"])
 @pytest.mark.parametrize("path", PATHS)
 def test_nan_reaches_the_rows_that_see_it(path, what, pattern):
     c = PATHS[path]()
@@ -100,3 +100,15 @@ def test_nan_reaches_the_rows_that_see_it(path, what, pattern):
     bad = check(c, clean, pattern)
     if pattern is ALL or what in ("query", "query inf", "page"):  # the others may lie below the window
         assert bool(bad.any())
+
+
+def test_a_nan_row_answers_the_same_whole_and_cut():
+    """The same sequence alone, where its items are whole, and in batches that cut them."""
+    got = []
+    for others in (0, 1, 40, 200):
+        c = Case([1] * (1 + others), [400] + [1 + 97 * b % 900 for b in range(others)], Hq=8, Hkv=2, seed=321)
+        c.q[0, 3, 0] = NAN
+        o, lse = c.run(ALL)
+        got.append(torch.isnan(o[0]))
+    for a in got:
+        assert a[3].all() and int(a.sum()) == c.D
