@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(384, 1)
             const bool begins = g->begins, whole = g->whole;
             const int slot = (2 * static_cast<int>(blockIdx.x) + (begins ? 1 : 0)) * R + x * 128 + row;
             const int parts = g->parts;
-            const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
+            const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
             const bool write = row < rows;
             const bool final = whole && p.acc == nullptr;
             // Rows leave through a small buffer of the warp, 64 bytes of each at a time, so that a store writes
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(384, 1)
             segs++;
             if (write) {
                 if (whole && p.acc == nullptr)
-                    p.lse[at] = l_sum > 0.f ? (m_ref + log2f(l_sum)) * 0.69314718055994530942f : -INFINITY;
+                    p.lse[at] = lse_of(m_ref, log2f(l_sum), l_sum);
                 else
                     (whole ? p.acc_ml[at] : p.part_ml[slot]) = make_float2(m_ref, l_sum);
                 if (begins && p.info != nullptr)

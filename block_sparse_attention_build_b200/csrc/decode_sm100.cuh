@@ -514,12 +514,12 @@ __global__ void __launch_bounds__(128, 2)
                         }
                     }
                 }
-                const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
+                const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
                 __nv_bfloat16* dst = p.o + t * p.o_token + hq * p.o_head + col;
 #pragma unroll
                 for (int i = 0; i < N; i++)
                     *reinterpret_cast<uint32_t*>(dst + i * 8) = pack_bf16x2(v[i][0] * inv, v[i][1] * inv);
-                if (first) p.lse[at] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
+                if (first) p.lse[at] = lse_of(m, __log2f(l), l);
             } else {
                 float* dst = (whole ? p.acc + at * D : p.part_o + static_cast<int64_t>(slot + r) * D) + col;
 #pragma unroll

@@ -103,6 +103,13 @@ struct PassParams {
 
 enum : int32_t { ST_PAGED_WAIT = 64 };
 
+// LSE of a row with maximum m (log2 units) and sum l: -inf where the row sees nothing (a sum of exactly 0), NaN
+// where a score is NaN or +inf (the sum is NaN then).
+__device__ __forceinline__ float lse_of(float m, float log2_l, float l)
+{
+    return l == 0.f ? -INFINITY : (m + log2_l) * 0.69314718055994530942f;
+}
+
 // One sequence as a pass sees it.
 struct SeqView {
     int32_t first;  // its first row in the token tensors
@@ -509,7 +516,7 @@ struct RowSum {
     template <class P>
     __device__ __forceinline__ void write(const P& p, uint32_t row, int lane) const
     {
-        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
         const uint32_t t = row / static_cast<uint32_t>(p.Hq), h = row - t * p.Hq;
         __nv_bfloat16* dst = p.o + t * p.o_token + h * p.o_head + lane * E;
         if constexpr (E == 4)
@@ -517,7 +524,7 @@ struct RowSum {
                 make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
         else
             *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-        if (lane == 0) p.lse[row] = L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+        if (lane == 0) p.lse[row] = lse_of(M, log2f(L), L);
     }
 };
 
@@ -634,14 +641,14 @@ __global__ void __launch_bounds__(256) join_tails_kernel(const TailJoinParams p)
             M = mn;
         }
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     const uint32_t tok = static_cast<uint32_t>(t.row) / static_cast<uint32_t>(p.Hq), h = t.row - tok * p.Hq;
     __nv_bfloat16* dst = p.o + tok * p.o_token + h * p.o_head + l * 4;
 #pragma unroll
     for (int x = 0; x < V; x++)
         *reinterpret_cast<uint2*>(dst + x * 32) = make_uint2(pack_bf16x2(acc[4 * x] * inv, acc[4 * x + 1] * inv),
                                                              pack_bf16x2(acc[4 * x + 2] * inv, acc[4 * x + 3] * inv));
-    if (l == 0) p.lse[t.row] = L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+    if (l == 0) p.lse[t.row] = lse_of(M, log2f(L), L);
 }
 
 }  // namespace sa

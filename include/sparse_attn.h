@@ -510,8 +510,9 @@ int sparse_attn_fwd_shared_workspace(int32_t T, int32_t Hq, int32_t Hkv, int32_t
  * SA_ERR_UNSUPPORTED).  Any number of new tokens per sequence, from single ones
  * to whole prompts, mixed freely.
  *   q, o  [T, Hq, D] bf16 by strides; o does not overlap q
- *   lse   [T, Hq] fp32 contiguous, natural log; rows that see nothing get O = 0,
- *         LSE = -inf
+ *   lse   [T, Hq] fp32 contiguous, natural log; rows that see nothing, or only scores
+ *         of -inf, get O = 0, LSE = -inf; rows that see a score of NaN or +inf (from an
+ *         infinity or NaN in the query or in a visible key) get NaN for both
  *   workspace  device memory of at least sparse_attn_fwd_cached_workspace bytes,
  *         256-byte aligned (SA_ERR_MISALIGNED; SA_ERR_BUFFER_TOO_SMALL), contents
  *         need not be preserved; not shared by calls that may run at the same time

@@ -1,5 +1,5 @@
-"""NaN and infinite scores in cached attention: a row that sees one has NaN for its output, on every
-path (items whole in a CTA or cluster, cut over CTAs or warps, over a prefix); the other rows keep
+"""NaN and infinite scores in cached attention: a row that sees one has NaN for its output and its LSE, on
+every path (items whole in a CTA or cluster, cut over CTAs or warps, over a prefix); the other rows keep
 their values."""
 import copy
 import math
@@ -82,6 +82,7 @@ def check(c, clean, pattern):
     T = L.shape[0]
     bad = torch.isnan(L) | torch.isposinf(L)
     o, lse = o[:T], lse[:T]
+    assert torch.equal(torch.isnan(lse), bad)
     assert torch.equal(torch.isnan(o).all(-1), bad) and torch.equal(torch.isnan(o).any(-1), bad)
     o[bad], lse[bad] = O0[bad].bfloat16(), L0[bad].float()
     clean.check(o, lse, pattern)
@@ -109,6 +110,6 @@ def test_a_nan_row_answers_the_same_whole_and_cut():
         c = Case([1] * (1 + others), [400] + [1 + 97 * b % 900 for b in range(others)], Hq=8, Hkv=2, seed=321)
         c.q[0, 3, 0] = NAN
         o, lse = c.run(ALL)
-        got.append(torch.isnan(o[0]))
-    for a in got:
-        assert a[3].all() and int(a.sum()) == c.D
+        got.append((torch.isnan(o[0]), torch.isnan(lse[0])))
+    for a, b in got:
+        assert a[3].all() and b[3] and int(a.sum()) == c.D and int(b.sum()) == 1
