@@ -153,7 +153,7 @@ int batch_status(const sa_cache_batch* b, const sa_kv_cache* c)
     if (b->B == 0 || b->T == 0) return SA_OK;
     if (!b->q_start || !b->kv_len || (b->max_pages > 0 && !b->table)) return SA_ERR_INVALID_ARG;
     if (b->B > 1 && b->table_stride < b->max_pages) return SA_ERR_INVALID_ARG;
-    if (int64_t(b->max_pages) * c->page_size > INT_MAX / 4) return SA_ERR_UNSUPPORTED;  // positions are 32 bits
+    if (int64_t(b->max_pages) * c->page_size > kMaxTokens) return SA_ERR_UNSUPPORTED;  // positions are 32 bits
     return SA_OK;
 }
 
@@ -225,7 +225,7 @@ extern "C" int sparse_attn_cache_append(const sa_view* k, const sa_view* v, cons
     if ((q == nullptr) != (q_out == nullptr) || (q && (!rotary || Hq < 0)) || pos_axis_stride < 0 || pos_offset < 0 ||
         (positions && !rotary))
         return SA_ERR_INVALID_ARG;
-    if (pos_offset > INT_MAX / 4) return SA_ERR_UNSUPPORTED;  // a token's position is 32 bits
+    if (pos_offset > kMaxTokens) return SA_ERR_UNSUPPORTED;  // a token's position is 32 bits
     const int32_t B = batch->B, T = batch->T, Hkv = cache->n_pages > 0 ? cache->Hkv : 0;
     const int32_t H = q ? Hq : 0;
     if (B == 0 || T == 0 || H + Hkv == 0) return SA_OK;
@@ -600,7 +600,7 @@ int fwd_paged(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* 
     if (!(scale > 0.f) || !std::isfinite(scale)) return SA_ERR_INVALID_ARG;
     if (int rc = check_pattern(*pattern)) return rc;
     if (pattern->causal != 1 || pattern->stride > 0 || pattern->area > 0) return SA_ERR_UNSUPPORTED;
-    if (prefix_len > INT_MAX / 4) return SA_ERR_UNSUPPORTED;
+    if (prefix_len > kMaxTokens) return SA_ERR_UNSUPPORTED;
     const int32_t T = batch->T;
     if (batch->B == 0 || T == 0 || Hq == 0) return SA_OK;
     if (cache->Hkv == 0 || cache->n_pages == 0 || Hq % cache->Hkv) return SA_ERR_UNSUPPORTED;
@@ -644,11 +644,12 @@ int fwd_paged(const sa_view* q, const sa_kv_cache* cache, const sa_cache_batch* 
     p.page_shift = page_shift_of(cache->page_size);
     p.max_pages = batch->max_pages;
     p.prefix_len = prefix_len;
-    // window and columns clipped to the longest possible sequence: the same keys, no overflow
-    const int64_t longest = prefix_len + int64_t(batch->max_pages) * cache->page_size;
-    p.window = clip_to(pattern->window, longest);
-    p.n_global = clip_to(pattern->n_global, longest);
-    p.cols = clip_to(pattern->sinks > pattern->n_global ? pattern->sinks : pattern->n_global, longest);
+    // window and global rows clipped to the farthest position, columns to the last key: the same keys, no overflow
+    const int64_t farthest = 2 * int64_t(kMaxTokens);
+    p.window = clip_to(pattern->window, farthest);
+    p.n_global = clip_to(pattern->n_global, farthest);
+    p.cols = clip_to(pattern->sinks > pattern->n_global ? pattern->sinks : pattern->n_global,
+                     prefix_len + int64_t(batch->max_pages) * cache->page_size);
     p.scale_log2 = scale * 1.44269504088896340736f;
     p.status = status;
     p.timeout = wait_limit_cycles();

@@ -118,10 +118,15 @@ struct SeqView {
     int32_t p0;     // position of its first new token, relative to its first key
 };
 
-// Tokens of sequence b in the cache: no more than its table has room for.
-__device__ __forceinline__ int cached_len(const PassParams& p, int b)
+// Tokens of a sequence as its kv_len gives them: where its new tokens stand.  The limit keeps a position behind a
+// prefix within 31 bits.
+constexpr int kMaxTokens = INT32_MAX / 4;
+__device__ __forceinline__ int tokens_of(int kv_len) { return min(max(kv_len, 0), kMaxTokens); }
+
+// Those of them that are in the cache: no more than the table has room for.
+__device__ __forceinline__ int cached_len(const PassParams& p, int tokens)
 {
-    return min(max(p.kv_len[b], 0), p.max_pages << p.page_shift);
+    return min(tokens, p.max_pages << p.page_shift);
 }
 
 __device__ __forceinline__ SeqView load_seq(const PassParams& p, int b)
@@ -136,8 +141,9 @@ __device__ __forceinline__ SeqView load_seq(const PassParams& p, int b)
         const int a = min(max(p.q_start[b], 0), p.T);
         s.first = a;
         s.m = max(min(p.q_start[b + 1], p.T) - a, 0);
-        s.len = cached_len(p, b);
-        s.p0 = s.len - s.m;
+        const int tokens = tokens_of(p.kv_len[b]);
+        s.len = cached_len(p, tokens);
+        s.p0 = tokens - s.m;
     }
     return s;
 }
@@ -210,7 +216,7 @@ __device__ __forceinline__ int token_position(const PassParams& p, int t)
             hi = mid;
     }
     const int first = p.q_start[lo], next = p.q_start[lo + 1];
-    return p.prefix_len + cached_len(p, lo) - (next - first) + (t - first);
+    return p.prefix_len + tokens_of(p.kv_len[lo]) - (next - first) + (t - first);
 }
 
 // Where a CTA is on the line of units.
@@ -275,7 +281,7 @@ __device__ __forceinline__ PassBounds pass_bounds(const PassParams& p)
 #pragma unroll 1
     for (int b = threadIdx.x % 32; b < p.B; b += 32) {
         const int m = p.q_start[b + 1] - p.q_start[b];
-        const int last = p.prefix_len + cached_len(p, b) - 1;
+        const int last = p.prefix_len + tokens_of(p.kv_len[b]) - 1;
         if (m <= 0) continue;
         lo = min(lo, last - m + 1);
         hi = max(hi, last);

@@ -19,6 +19,8 @@
 
 #include <cstdint>
 
+#include "paged_sm100.cuh"
+
 namespace sa {
 
 constexpr int kMaxPairs = 64;  // D / 2
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(kRotThreads, rot_blocks(LAYOUT)) rotary_kernel
         b = max(cnt - 1, 0);
         const int first = p.q_start[b], next = p.q_start[b + 1];
         n = t;
-        place = p.kv_len[b] - (next - first) + static_cast<int>(t - first);
+        place = tokens_of(p.kv_len[b]) - (next - first) + static_cast<int>(t - first);
         const int pi = place >> p.page_shift;
         if (have && place >= 0 && pi < p.max_pages) {
             const int page = p.table[b * p.table_stride + pi];

@@ -467,10 +467,12 @@ typedef struct {
  *                    to no sequence, are not read and keep their outputs
  *   max_q            most new tokens of one sequence as far as the host knows (0:
  *                    unknown); chooses between kernels, results hold for any value
- * Row i of sequence b stands at position kv_len[b] - (its new tokens) + i.  A
- * kv_len above max_pages * page_size is read as that.  Table entries beyond a
- * sequence's length are not read; a page outside [0, n_pages) holds keys and
- * values of zero and takes no writes.
+ * Row i of sequence b stands at position kv_len[b] - (its new tokens) + i, in every
+ * call.  A kv_len above max_pages * page_size moves no row: tokens whose place lies
+ * behind the table are not in the cache (the append drops them, no row sees them).
+ * A kv_len below 0 is read as 0, one of 2^29 or more as 2^29 - 1.  Table entries
+ * beyond a sequence's length are not read; a page outside [0, n_pages) holds keys
+ * and values of zero and takes no writes.
  */
 typedef struct {
     int32_t B, T, max_q, max_pages;
