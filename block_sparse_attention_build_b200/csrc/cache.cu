@@ -404,10 +404,12 @@ int launch_decode(const sa_kv_cache& cache, const PassParams& p, const DecodePla
 {
     if (plan.mt == 1)
         return plan.mode == kWarps      ? launch_decode_as<D, 1, kWarps>(cache, p, plan, st)
+               : plan.mode == kBoth     ? launch_decode_as<D, 1, kBoth>(cache, p, plan, st)
                : plan.mode == kClusters ? launch_decode_as<D, 1, kClusters>(cache, p, plan, st)
                                         : launch_decode_as<D, 1, kLine>(cache, p, plan, st);
-    return plan.mode == kClusters ? launch_decode_as<D, 2, kClusters>(cache, p, plan, st)
-                                  : launch_decode_as<D, 2, kLine>(cache, p, plan, st);
+    return plan.mode == kBoth       ? launch_decode_as<D, 2, kBoth>(cache, p, plan, st)
+           : plan.mode == kClusters ? launch_decode_as<D, 2, kClusters>(cache, p, plan, st)
+                                    : launch_decode_as<D, 2, kLine>(cache, p, plan, st);
 }
 
 template <int D>
@@ -514,6 +516,30 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
     };
     const bool finished = rows <= kDecodeRows && plan.mode == kClusters &&
                           (!prefix || whole_over || parts_over() <= 16);
+    // Both passes in one launch where each is whole items by clusters and the sequences' fit beside the prefix's:
+    // in the prefix's clusters, or a CTA to each of few units.
+    if (whole_over && rows <= kDecodeRows && over.ctas < held) {
+        DecodePlan own = plan_decode<D>(most_keys(room, most_q), p.B, rows, p.Hkv, held - over.ctas, false);
+        const int64_t items = int64_t(p.B) * p.Hkv, units = most_keys(room, most_q) / DecodeCfg<D, 1>::UK + 3;
+        const int64_t c = own.cluster > 1 && items * over.cluster <= held - over.ctas ? over.cluster : 1;
+        if (own.mode == kClusters && (units + c - 1) / c <= 6) {
+            const int64_t ctas = std::min(items * c, held - over.ctas);
+            own.mt = over.mt;  // of all rows: no less than the sequences' own
+            own.mode = kBoth;
+            own.cluster = over.cluster;
+            own.ctas = over.ctas + (ctas + over.cluster - 1) / over.cluster * over.cluster;
+            use_parts(p, w, ws, 1, w.rows_decode + w.rows_chunk, D, true);
+            p.side_ctas = static_cast<int32_t>(over.ctas);
+            p.cluster = static_cast<int32_t>(c);
+            p.side_table = prefix_table;
+            p.side_info = p.info;
+            p.side_acc = p.acc;
+            p.side_ml = p.acc_ml;
+            use_parts(p, w, ws, 0, 0, D, true);
+            if (int rc = launch_decode<D>(cache, p, own, st)) return rc;
+            return launch_join<D>(j, true, st);
+        }
+    }
     if (prefix) {
         // the rows of all sequences against the prefix
         PassParams pp = p;

@@ -90,6 +90,12 @@ struct PassParams {
     TailRow* tails;            // [CTAs * R]
     float* acc;                // null: finished rows go to o and lse; else [T, Hq, D] unnormalised,
     float2* acc_ml;            // [T, Hq]
+    int32_t side_ctas;         // kBoth: the launch's first CTAs, which run the pass over the prefix, with these
+    int32_t cluster;           // in place of over_prefix, table, info, acc; CTAs that share an item of the others
+    const int32_t* side_table;
+    RowInfo* side_info;
+    float* side_acc;
+    float2* side_ml;
     const float* pre_acc;      // not null: what the pass over the prefix left, added to every row
     const float2* pre_ml;
     const RowInfo* pre_info;   // not null: rows of that pass may lie in parts instead, of the arrays

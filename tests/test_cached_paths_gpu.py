@@ -113,3 +113,30 @@ def test_two_host_threads():
         assert len(got[i]) == 50
         for a, b in got[i]:
             assert torch.equal(a, want[i][0]) and torch.equal(b, want[i][1])
+
+
+# (q_len, kv_len, Hq, Hkv, prefix): sequences a CTA each beside clusters over the prefix, several to a CTA; in the
+# prefix's clusters; up to 16 rows in all, and up to 32; no token, no key, padded sequences
+BOTH = [([1] * 8, [128, 1, 77, 30, 0, 64, 65, 3], 16, 16, 2043), ([1], [600], 2, 2, 1500), ([1, 1], [300, 40], 8, 1, 900),
+        ([1] * 8, [9 * b for b in range(8)], 32, 8, 1000), ([4, 3, 0, 1], [200, 3, 9, 60], 8, 4, 300),
+        ([16], [16], 2, 1, 64), ([2, 5], [2, 5], 4, 1, 17), ([1] * 31, [1 + b for b in range(31)], 3, 3, 130)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("pattern", [ALL, sa.Pattern(window=150, sinks=5), sa.Pattern(window=3, n_global=40)],
+                         ids=["all", "w150s5", "w3g40"])
+@pytest.mark.parametrize("case", BOTH, ids=[f"both{i}" for i in range(len(BOTH))])
+def test_short_prefixes_beside_their_sequences(case, pattern, D):
+    """Few rows in all behind a prefix of few keys: both passes in one launch, captured and replayed too."""
+    q_len, kv_len, Hq, Hkv, prefix = case
+    c = Case(q_len, kv_len, Hq=Hq, Hkv=Hkv, D=D, page=32, prefix=prefix, pad_rows=1, seed=506)
+    o, lse = go(c, pattern)
+    args = (c.dev(c.q), c.cache(), c.batch(max(q_len)), c.dev(c.prefix_table), prefix, pattern)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = [sa.fwd_shared(*args) for _ in range(2)]  # a workspace each, out of the graph's pool
+    for _ in range(2):
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in got:
+            assert torch.equal(a[:len(o)], o) and torch.equal(b[:len(lse)], lse)
