@@ -180,8 +180,12 @@ class CacheBatch:
     """A batch over a cache: ``q_start`` [B + 1] rows of the token tensors where each sequence's
     new tokens begin (ascending from 0), ``kv_len`` [B] cached tokens (new ones included),
     ``table`` [B, max_pages] pages.  int32 CUDA tensors; their contents are read when a kernel
-    runs, so a captured graph follows them.  ``max_q``: most new tokens of one sequence, as far as
-    known; it only chooses between kernels."""
+    runs, so a captured graph follows them.  Tokens whose place lies behind the table are not in the
+    cache.  ``max_q``: most new tokens of one sequence, as far as known.  Results do not depend on
+    it, the choice of kernels does: left out, the average is taken, and a long piece among many
+    single tokens then runs on the kernel for few rows (255 single tokens and a piece of 512, 32/8
+    heads of 128: 224 us with ``max_q=512``, 442 without).  Give it where pieces and single tokens
+    mix."""
 
     def __init__(self, q_start, kv_len, table, max_q: int | None = None):
         dev = q_start.device
@@ -345,8 +349,9 @@ def _attend(fn, where, q, cache, batch, prefix, pattern, scale, out, lse, worksp
     elif workspace.device != dev or not workspace.is_contiguous():
         raise TypeError(f"{where}: workspace must be a contiguous tensor on {dev}")
     _call(fn, where, dev, stream, _tokens(q, st), cache._ref, batch._c(T), *prefix,
-          _pack_pattern(p.causal, p.window, p.sinks, p.stride, p.n_global, p.area, p.summary), Hq, scale if scale is not None else 1.0 / math.sqrt(D), ov, lse.data_ptr(),
-          workspace.data_ptr(), workspace.nbytes)
+          _pack_pattern(p.causal, p.window, p.sinks, p.stride, p.n_global, p.area, p.summary), Hq,
+          scale if scale is not None else 1.0 / math.sqrt(D), ov, lse.data_ptr(), workspace.data_ptr(),
+          workspace.nbytes)
     return out, lse
 
 
@@ -355,9 +360,11 @@ def fwd_cached(q, cache: KVCache, batch: CacheBatch, pattern: Pattern, scale: fl
     """Attention of new tokens q [T, Hq, D] over the cache: O [T, Hq, D] bf16 and LSE [T, Hq] fp32.
 
     ``pattern`` is causal with window, sinks and n_global.  Rows of no sequence keep what ``out``
-    and ``lse`` held.  ``workspace``: at least ``fwd_cached_workspace_bytes`` bytes, not shared by
+    and ``lse`` held; rows that see nothing get 0 and -inf, rows that see a score of NaN or +inf get
+    NaN for both.  ``workspace``: at least ``fwd_cached_workspace_bytes`` bytes, not shared by
     calls that may run at the same time.  Asynchronous on ``stream``."""
-    return _attend(lib.sparse_attn_fwd_cached, "fwd_cached", q, cache, batch, (), pattern, scale, out, lse, workspace, stream)
+    return _attend(lib.sparse_attn_fwd_cached, "fwd_cached", q, cache, batch, (), pattern, scale, out, lse, workspace,
+                   stream)
 
 
 def fwd_shared(q, cache: KVCache, batch: CacheBatch, prefix_table, prefix_len: int, pattern: Pattern,

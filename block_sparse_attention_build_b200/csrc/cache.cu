@@ -505,8 +505,8 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
     const DecodePlan plan = plan_decode<D>(most_keys(room, most_q), p.B, rows, p.Hkv, held, by_warps);
     // Nothing is left for join_kernel where each item is finished by its CTAs; over a prefix the sequences'
     // pass then adds what the prefix's left: whole rows, or the parts of cut ones where these are few (122 rows a
-    // head behind 151 tokens, 2 parts: 25.2 us with join_kernel, 21.4 without; 12 sequences behind 1223, 15 parts:
-    // 23.0 and 21.4; behind 12230, 20 parts: 31.2 and 34.1).
+    // head behind 151 tokens, 2 parts: 28.0 us on the device with join_kernel, 25.7 without; 12 sequences behind
+    // 1223, 15 parts: 23.7 and 23.5; behind 12230, 20 parts: 33.4 and 35.0).
     auto parts_over = [&]() {
         const bool few = all_rows <= kDecodeRows;
         const int64_t R = few ? 16 * over.mt : ChunkCfg<D>::R, ctas = few ? over.ctas : device_sm_count();
@@ -517,7 +517,9 @@ int run_paged(const sa_kv_cache& cache, PassParams p, const JoinParams& j, const
     const bool finished = rows <= kDecodeRows && plan.mode == kClusters &&
                           (!prefix || whole_over || parts_over() <= 16);
     // Both passes in one launch where each is whole items by clusters and the sequences' fit beside the prefix's:
-    // in the prefix's clusters, or a CTA to each of few units.
+    // in the prefix's clusters, or a CTA to each of few units.  On the device, one after another and like this (24
+    // calls of 1 to 32 rows, none slower): 2 sequences behind 200 tokens, 1 head of 64, 11.1 and 7.5 us; 4 behind
+    // 1000, 64/16 heads of 128, 15.9 and 12.0; 8 behind 2043, 16 heads of 128, 18.2 and 13.2.
     if (whole_over && rows <= kDecodeRows && over.ctas < held) {
         DecodePlan own = plan_decode<D>(most_keys(room, most_q), p.B, rows, p.Hkv, held - over.ctas, false);
         const int64_t items = int64_t(p.B) * p.Hkv, units = most_keys(room, most_q) / DecodeCfg<D, 1>::UK + 3;

@@ -20,11 +20,10 @@
 // by join_kernel.  kClusters, for items of few units: a cluster of CTAs takes whole
 // items, its CTAs every n-th unit of one, and the parts are added over distributed
 // shared memory, so that nothing has to follow.  kBoth: the same for two passes side by
-// side, that over a prefix and that of the sequences, each by CTAs of its own (8 sequences
-// behind 2043 tokens: 18.4 us on the device one after another, 13.2 like this, join_kernel
-// included).  kWarps, for many short items: the line
-// is cut evenly over the warps, which never meet, so that an item's end costs no
-// barrier and no idle warps.
+// side, that over a prefix and that of the sequences, each by CTAs of its own, added by
+// join_kernel (8 sequences behind 2043 tokens: 13.2 us on the device, one after another
+// 18.2).  kWarps, for many short items: the line is cut evenly over the warps, which never
+// meet, so that an item's end costs no barrier and no idle warps.
 //
 // Code that runs once in a launch costs about 9 cycles an instruction (it comes
 // from L2: measured on the first and second pass over the same tile, 8660 and 1580
@@ -290,7 +289,8 @@ __global__ void __launch_bounds__(128, 2)
             const bool look_up = p.over_prefix && !(p_lo >= p.prefix_len - 1 && p.window >= 0 && p_hi <= p.window);
             if constexpr (MT == 2) {
                 // 32 rows' fragments would take 64 registers, and what spilled was read for every tile (32 sequences
-                // of up to 16384 keys, 32 rows a head: 295 us so, 138 like this).  To shared memory, chunks of 16
+                // of up to 16384 keys, 32 rows a head: 295 us so, 134 like this; 20 to 112 bytes still spill at head
+                // size 128).  To shared memory, chunks of 16
                 // bytes swizzled; every warp is past the barriers of the item before.
 #pragma unroll 1
                 for (int c = tid; c < R * (D / 8); c += C::kThreads) {

@@ -466,7 +466,9 @@ typedef struct {
  *   T                rows of the token tensors; rows q_start[B] .. T - 1 belong
  *                    to no sequence, are not read and keep their outputs
  *   max_q            most new tokens of one sequence as far as the host knows (0:
- *                    unknown); chooses between kernels, results hold for any value
+ *                    unknown, the average is taken); chooses between kernels.
+ *                    Results hold for any value; one far too low is slow, since a
+ *                    long piece then runs on the kernel for few rows
  * Row i of sequence b stands at position kv_len[b] - (its new tokens) + i, in every
  * call.  A kv_len above max_pages * page_size moves no row: tokens whose place lies
  * behind the table are not in the cache (the append drops them, no row sees them).
